@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the layer runs in the library's HIP
 kernels. PyTorch supplies device memory and the current stream. The names
 mirror the C ABI in include/moe_mxfp4.h: query, workspace_layout, forward,
-strerror. There is no fallback: without the built library every call raises.
+strerror; the operators of include/moe_ops.h (dispatch, combine, 4-bit products) are in ops.py and
+exported here. There is no fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
@@ -13,7 +14,8 @@ from dataclasses import dataclass
 
 __all__ = ["Shape", "query", "workspace_layout", "forward", "forward_timed", "forward_noalloc",
            "strerror", "lib_path", "MoeError", "read_maps", "ADTYPE", "GEMM2_PATH", "load_library",
-           "prepack"]
+           "prepack", "DispatchShape", "W4Shape", "dispatch_query", "dispatch", "dispatch_backward",
+           "combine", "combine_backward", "w4_linear", "w4_grouped_linear"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoe_mxfp4.so")
@@ -287,3 +289,7 @@ def read_maps(workspace, shape: Shape) -> dict:
         maps["xs"] = view(L["xs"], T * shape.H // 32, torch.uint8).view(T, shape.H // 32)
         maps["act_scales"] = view(L["act_scales"], L["rows_pad"] * shape.I // 32, torch.uint8)
     return maps
+
+
+from .ops import (DispatchShape, W4Shape, combine, combine_backward, dispatch,  # noqa: E402
+                  dispatch_backward, dispatch_query, w4_grouped_linear, w4_linear)

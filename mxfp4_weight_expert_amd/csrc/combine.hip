@@ -1,0 +1,146 @@
+// Combine: expert rows weighted and summed back to token order, and its
+// gradients. Each row and each token is read or written once; memory bounds
+// all three. Sums are 32-bit, in an order fixed by the sizes (no atomics).
+#include "rows.h"
+#include "kernels.h"
+
+#include <type_traits>
+
+namespace moe {
+
+// out[t] = sum over k of w[t, k] * rows[row(t, k)] (w = nullptr: 1, the
+// gradient of dispatch). A one-wave block takes 64 16-byte pieces of one
+// token; it first packs the token's rows and weights into LDS in ascending k,
+// so the sum has no branches and its loads go out eight at a time.
+template <int DT>
+__global__ __launch_bounds__(64) void combine_kernel(const uint8_t* __restrict__ rows,
+                                                     const int32_t* __restrict__ slot_row,
+                                                     const float* __restrict__ topk_w, int topk,
+                                                     int nslots, int H, int npiece,
+                                                     uint8_t* __restrict__ out) {
+  using R = Row<DT>;
+  constexpr int V = R::kVec;
+  __shared__ int32_t s_row[kMaxTopK];
+  __shared__ float s_w[kMaxTopK];
+  const int t = blockIdx.x / npiece;
+  const int c = (blockIdx.x - t * npiece) * kWave + lane_id();
+  const int k = lane_id();
+  const size_t slot = static_cast<size_t>(t) * topk + k;
+  const int row = k < topk ? slot_row[slot] : -1;
+  const bool valid = static_cast<uint32_t>(row) < static_cast<uint32_t>(nslots);
+  const uint64_t m = ballot(valid);
+  if (valid) {
+    const int pos = popc_below(m);
+    s_row[pos] = row;
+    s_w[pos] = topk_w != nullptr ? topk_w[slot] : 1.0f;
+  }
+  __syncthreads();
+  const int n = __popcll(m);
+  const int nvec = H / V;
+  const size_t row_bytes = static_cast<size_t>(H) * R::kSize;
+  const uint8_t* src = rows + 16 * static_cast<size_t>(c);
+  uint8_t* dst = out + static_cast<size_t>(t) * row_bytes + 16 * static_cast<size_t>(c);
+  if (c < nvec) {
+    float acc[V], f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (k0 + u < n) v[u] = ld16_any<true>(src + s_row[k0 + u] * row_bytes);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (k0 + u < n) {
+          R::unpack(v[u], f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += s_w[k0 + u] * f[i];
+        }
+      }
+    }
+    st16_any<false>(dst, R::pack(acc));
+  } else if (c == nvec) {
+    for (int i = 0; i < H - nvec * V; ++i) {
+      float acc = 0.0f;
+      for (int u = 0; u < n; ++u) acc += s_w[u] * R::get(src + s_row[u] * row_bytes + i * R::kSize);
+      R::put(dst + i * R::kSize, acc);
+    }
+  }
+}
+
+// Gradients of combine: a wave per slot writes w * dout[t] to the slot's row
+// and reduces <dout[t], row> over its lanes.
+template <int DT>
+__global__ __launch_bounds__(256) void combine_backward_kernel(
+    const uint8_t* __restrict__ dout, const uint8_t* __restrict__ rows,
+    const int32_t* __restrict__ slot_row, const float* __restrict__ topk_w, int topk, int nslots,
+    int H, uint8_t* __restrict__ drows, float* __restrict__ dtopk_w) {
+  using R = Row<DT>;
+  constexpr int V = R::kVec;
+  const int s = blockIdx.x * 4 + wave_index();
+  if (s >= nslots) return;
+  const int lane = lane_id();
+  const int row = slot_row[s];
+  if (static_cast<uint32_t>(row) >= static_cast<uint32_t>(nslots)) {
+    if (lane == 0) dtopk_w[s] = 0.0f;
+    return;
+  }
+  const float w = topk_w[s];
+  const size_t row_bytes = static_cast<size_t>(H) * R::kSize;
+  const uint8_t* g = dout + static_cast<size_t>(s / topk) * row_bytes;
+  const uint8_t* y = rows + row * row_bytes;
+  uint8_t* d = drows + row * row_bytes;
+  const int nvec = H / V;
+  float dot = 0.0f;
+  for (int c = lane; c < nvec; c += kWave) {
+    const size_t at = 16 * static_cast<size_t>(c);
+    float fg[V], fy[V];
+    R::unpack(ld16_any<false>(g + at), fg);
+    R::unpack(ld16_any<false>(y + at), fy);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dot += fg[i] * fy[i];
+      fg[i] *= w;
+    }
+    st16_any<false>(d + at, R::pack(fg));
+  }
+  const int i = nvec * V + lane;
+  if (i < H) {
+    const size_t at = static_cast<size_t>(i) * R::kSize;
+    const float fg = R::get(g + at);
+    dot += fg * R::get(y + at);
+    R::put(d + at, w * fg);
+  }
+  dot = wave_sum_f(dot);
+  if (lane == 0) dtopk_w[s] = dot;
+}
+
+namespace {
+template <class F>
+hipError_t by_dtype(int dtype, F f) {
+  if (dtype == MOE_DTYPE_BF16) f(std::integral_constant<int, MOE_DTYPE_BF16>{});
+  else if (dtype == MOE_DTYPE_FP16) f(std::integral_constant<int, MOE_DTYPE_FP16>{});
+  else f(std::integral_constant<int, MOE_DTYPE_FP32>{});
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
+  return by_dtype(a.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const int npiece = (a.H + Row<DT>::kVec * kWave - 1) / (Row<DT>::kVec * kWave);
+    hipLaunchKernelGGL((combine_kernel<DT>), dim3(static_cast<unsigned>(a.T) * npiece), dim3(64), 0,
+                       st, a.rows, a.slot_row, a.topk_w, a.topk, a.T * a.topk, a.H, npiece, a.out);
+  });
+}
+
+hipError_t launch_combine_backward(const CombineArgs& a, hipStream_t st) {
+  return by_dtype(a.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const int nslots = a.T * a.topk;
+    hipLaunchKernelGGL((combine_backward_kernel<DT>), dim3((nslots + 3) / 4), dim3(256), 0, st,
+                       a.dout, a.rows, a.slot_row, a.topk_w, a.topk, nslots, a.H, a.out, a.dtopk_w);
+  });
+}
+
+}  // namespace moe

@@ -1,0 +1,154 @@
+// Dispatch: token rows into expert order. Slot s = t * topk + k with local
+// expert e(s) goes to row
+//   row(s) = #{s' : e(s') < e(s)} + #{s' < s : e(s') = e(s)},
+// so rows follow the experts and, within one, the slots, whatever order the
+// blocks run in. What it cannot do without: the ids, each token once, each
+// row once; memory bounds it.
+#include "rows.h"
+#include "kernels.h"
+
+namespace moe {
+
+// Local expert of a global id, or -1.
+__device__ __forceinline__ int local_expert(int id, int offset, int E) {
+  return id >= offset && id - offset < E ? id - offset : -1;
+}
+
+// One wave copies a row of `bytes` (a multiple of 2).
+__device__ __forceinline__ void wave_copy_row(const uint8_t* src, uint8_t* dst, uint32_t bytes) {
+  const uint32_t n = bytes >> 4, lane = lane_id();
+  uint32_t c = lane;
+  for (; c + 192 < n; c += 256) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = ld16_any<false>(src + 16 * static_cast<size_t>(c + 64 * u));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) st16_any<false>(dst + 16 * static_cast<size_t>(c + 64 * u), v[u]);
+  }
+  for (; c < n; c += 64)
+    st16_any<false>(dst + 16 * static_cast<size_t>(c), ld16_any<false>(src + 16 * static_cast<size_t>(c)));
+  const uint32_t at = (n << 4) + 2 * lane;
+  if (at < bytes)
+    *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(src + at);
+}
+
+// Few slots: one launch. Every block reads all ids and keys slot s by
+// (expert, s), expert E for slots without one; a wave counts the keys below
+// its slot's, which is its row, and copies the token there. The last block
+// counts the slots of each expert and scans the counts.
+__global__ __launch_bounds__(256) void dispatch_fused_kernel(
+    const uint8_t* __restrict__ x, const int32_t* __restrict__ ids, int nslots, int topk, int E,
+    int expert_offset, uint32_t row_bytes, uint8_t* __restrict__ rows,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_slot, int32_t* __restrict__ slot_row) {
+  __shared__ uint32_t s_key[kFusedSlots];
+  __shared__ int s_wave[4];
+  const int tid = threadIdx.x, lane = lane_id(), w = wave_index();
+  if (blockIdx.x == gridDim.x - 1) {
+    int* cnt = reinterpret_cast<int*>(s_key);  // kMaxExperts counters
+    for (int e = tid; e < kMaxExperts; e += 256) cnt[e] = 0;
+    __syncthreads();
+    for (int s = tid; s < nslots; s += 256) {
+      const int e = local_expert(ids[s], expert_offset, E);
+      if (e >= 0) atomicAdd(&cnt[e], 1);  // whole numbers: the order changes nothing
+    }
+    __syncthreads();
+    constexpr int kPer = kMaxExperts / 256;
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      c[i] = cnt[tid * kPer + i];
+      sum += c[i];
+    }
+    const int incl = wave_incl_scan(sum);
+    if (lane == kWave - 1) s_wave[w] = incl;
+    __syncthreads();
+    int at = incl - sum;
+    for (int i = 0; i < w; ++i) at += s_wave[i];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      if (e <= E) offsets[e] = at;  // counters from E on are 0: offsets[E] is the total
+      at += c[i];
+    }
+    if (E == kMaxExperts && tid == 255) offsets[E] = at;
+    return;
+  }
+  for (int s = tid; s < nslots; s += 256) {
+    const int e = local_expert(ids[s], expert_offset, E);
+    s_key[s] = static_cast<uint32_t>(e >= 0 ? e : E) * kFusedSlots + s;
+  }
+  __syncthreads();
+  const int s = blockIdx.x * 4 + w;
+  if (s >= nslots) return;
+  const uint32_t key = s_key[s];
+  if (key >= static_cast<uint32_t>(E) * kFusedSlots) {
+    if (lane == 0) slot_row[s] = -1;
+    return;
+  }
+  int row = 0;
+  for (int i = 0; i < nslots; i += kWave)
+    row += __popcll(ballot(i + lane < nslots && s_key[min(i + lane, nslots - 1)] < key));
+  if (lane == 0) {
+    slot_row[s] = row;
+    row_slot[row] = s;
+  }
+  wave_copy_row(x + static_cast<size_t>(s / topk) * row_bytes,
+                rows + static_cast<size_t>(row) * row_bytes, row_bytes);
+}
+
+// Many slots: the maps come from the sort's range kernels (launch_sort_maps);
+// then a one-wave block takes 1 KB of a token, reads it once and writes it to
+// the token's rows.
+__global__ __launch_bounds__(64) void dispatch_copy_kernel(const uint8_t* __restrict__ x,
+                                                           const int32_t* __restrict__ slot_row,
+                                                           int topk, uint32_t row_bytes, int npiece,
+                                                           uint8_t* __restrict__ rows) {
+  const int t = blockIdx.x / npiece;
+  const uint32_t c = (blockIdx.x - t * npiece) * kWave + lane_id();
+  const uint32_t n = row_bytes >> 4, tail = row_bytes & 15;
+  const uint8_t* src = x + static_cast<size_t>(t) * row_bytes + 16 * static_cast<size_t>(c);
+  const int32_t* map = slot_row + static_cast<size_t>(t) * topk;
+  uint4 v = {0, 0, 0, 0};
+  if (c < n) v = ld16_any<false>(src);
+  for (int k = 0; k < topk; ++k) {
+    const int row = map[k];
+    if (row < 0) continue;
+    uint8_t* dst = rows + static_cast<size_t>(row) * row_bytes + 16 * static_cast<size_t>(c);
+    if (c < n) {
+      st16_any<false>(dst, v);
+    } else if (c == n) {
+      for (uint32_t b = 0; b < tail; b += 2)
+        *reinterpret_cast<uint16_t*>(dst + b) = *reinterpret_cast<const uint16_t*>(src + b);
+    }
+  }
+}
+
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
+  const uint32_t row_bytes = static_cast<uint32_t>(a.H) * a.elem;
+  const int nslots = a.T * a.topk;
+  if (nslots <= kFusedSlots) {
+    hipLaunchKernelGGL(dispatch_fused_kernel, dim3((nslots + 3) / 4 + 1), dim3(256), 0, st, a.x,
+                       a.ids, nslots, a.topk, a.E, a.expert_offset, row_bytes, a.rows, a.offsets,
+                       a.row_slot, a.slot_row);
+    return hipGetLastError();
+  }
+  SortMapsArgs m;
+  m.ids = a.ids;
+  m.nslots = nslots;
+  m.E = a.E;
+  m.expert_offset = a.expert_offset;
+  m.n_ranges = (nslots + kRangeSlots - 1) / kRangeSlots;
+  m.range_counts = a.range_counts;
+  m.counts = a.counts;
+  m.offsets = a.offsets;
+  m.sorted_slot = a.row_slot;
+  m.expanded_idx = a.slot_row;
+  const hipError_t err = launch_sort_maps(m, st);
+  if (err != hipSuccess) return err;
+  const int npiece = static_cast<int>((row_bytes + 1023) / 1024);
+  hipLaunchKernelGGL(dispatch_copy_kernel, dim3(static_cast<unsigned>(a.T) * npiece), dim3(64), 0,
+                     st, a.x, a.slot_row, a.topk, row_bytes, npiece, a.rows);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -89,6 +89,62 @@ struct FinalizeArgs {
   uint16_t* out;
 };
 hipError_t launch_finalize(const FinalizeArgs& a, hipStream_t st);
+
+// Maps of the dispatch operator from global ids: the sort's kernels for many
+// slots, without the layer's chunk tables and gate.
+struct SortMapsArgs {
+  const int32_t* ids;  // [nslots] global ids
+  int nslots, E, expert_offset, n_ranges;
+  int32_t* range_counts;  // [n_ranges, E]
+  int32_t* counts;        // [E]
+  int32_t* offsets;       // [E + 1]
+  int32_t* sorted_slot;   // [nslots]
+  int32_t* expanded_idx;  // [nslots]
+};
+hipError_t launch_sort_maps(const SortMapsArgs& a, hipStream_t st);
+
+// Slots up to which dispatch is one launch (dispatch.hip).
+constexpr int kFusedSlots = 4096;
+struct DispatchArgs {
+  const uint8_t* x;    // [T, H]
+  const int32_t* ids;  // [T, topk]
+  int T, E, topk, H, expert_offset;
+  int elem;  // bytes of an element
+  uint8_t* rows;
+  int32_t* offsets;
+  int32_t* row_slot;
+  int32_t* slot_row;
+  int32_t* range_counts;  // workspace of the many-slot path, as in SortMapsArgs
+  int32_t* counts;
+};
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st);
+
+struct CombineArgs {
+  const uint8_t* dout;  // [T, H] (backward)
+  const uint8_t* rows;  // [T * topk, H]
+  const int32_t* slot_row;
+  const float* topk_w;  // null: 1 (forward only)
+  int T, topk, H, dtype;
+  uint8_t* out;    // [T, H], backward: drows [T * topk, H]
+  float* dtopk_w;  // backward
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
+hipError_t launch_combine_backward(const CombineArgs& a, hipStream_t st);
+
+struct W4Args {
+  const void* x;           // [M, K], rows ldx apart
+  const int32_t* offsets;  // [E + 1] (grouped) or null
+  const uint8_t* w;        // [E, Np, K / 2] packed
+  const void* scales;      // [E, N, K / group]
+  const uint8_t* zeros;    // [E, N, K / group] or null
+  const void* bias;        // [E, N] or null
+  void* out;               // [M, N], rows ldo apart
+  int M, N, K, E, format, group, dtype, out_dtype;
+  int64_t ldx, ldo;
+  int kw;  // waves of a block that split K (set by the launcher)
+};
+hipError_t launch_w4(const W4Args& a, hipStream_t st);
+
 hipError_t launch_prepack(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t row_bytes,
                           hipStream_t st);
 

@@ -262,10 +262,25 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(
 }
 
 // ------------------------------------------------------------ large shapes
+// Where the range kernels read a slot's expert: the layer's local ids as they
+// are, or global ids (dispatch), whose local id is -1 outside the range.
+struct LocalIds {
+  const int32_t* ids;
+  __device__ __forceinline__ int operator()(int s) const { return ids[s]; }
+};
+struct GlobalIds {
+  const int32_t* ids;
+  int offset, E;
+  __device__ __forceinline__ int operator()(int s) const {
+    const int id = ids[s];
+    return id >= offset && id - offset < E ? id - offset : -1;
+  }
+};
+
 // One wave per block (ranges spread over the CUs): range r's expert
 // histogram in LDS, written range-major to range_counts[r][Ep].
-__global__ __launch_bounds__(64) void sort_count_kernel(const int32_t* __restrict__ slot_expert,
-                                                        int nslots, int Ep, int n_ranges,
+template <class Ids>
+__global__ __launch_bounds__(64) void sort_count_kernel(const Ids slot_expert, int nslots, int Ep, int n_ranges,
                                                         int32_t* __restrict__ range_counts) {
   extern __shared__ int32_t lds[];
   const int lane = lane_id();
@@ -276,7 +291,7 @@ __global__ __launch_bounds__(64) void sort_count_kernel(const int32_t* __restric
   const int s0 = r * kRangeSlots;
   const int s1 = min(nslots, s0 + kRangeSlots);
   for (int s = s0 + lane; s < s1; s += kWave) {
-    const int e = slot_expert[s];
+    const int e = slot_expert(s);
     if (e >= 0) atomicAdd(&h[e], 1);
   }
   __builtin_amdgcn_wave_barrier();
@@ -355,8 +370,9 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(int Ep, int B, int forc
                       dense_tiles, nullptr);
 }
 
+template <class Ids>
 __global__ __launch_bounds__(64) void sort_scatter_kernel(
-    const int32_t* __restrict__ slot_expert, int nslots, int Ep, int n_ranges, int key_bits,
+    const Ids slot_expert, int nslots, int Ep, int n_ranges, int key_bits,
     const int32_t* __restrict__ range_base, const int32_t* __restrict__ offsets,
     int32_t* __restrict__ sorted_slot, int32_t* __restrict__ expanded_idx) {
   constexpr int kGroups = kRangeSlots / kWave;
@@ -368,7 +384,7 @@ __global__ __launch_bounds__(64) void sort_scatter_kernel(
   // the range's experts, all loads in flight at once (clamped index)
   int ex[kGroups];
 #pragma unroll
-  for (int gi = 0; gi < kGroups; ++gi) ex[gi] = slot_expert[min(s0 + gi * kWave + lane, nslots - 1)];
+  for (int gi = 0; gi < kGroups; ++gi) ex[gi] = slot_expert(min(s0 + gi * kWave + lane, nslots - 1));
   int32_t* next = lds;  // next free row per expert for this range
   for (int i = lane; i < Ep; i += kWave)
     next[i] = offsets[i] + range_base[static_cast<size_t>(r) * Ep + i];
@@ -393,7 +409,8 @@ hipError_t launch_sort_and_gate(const SortArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   const size_t lds = static_cast<size_t>(a.Ep) * sizeof(int32_t);
-  hipLaunchKernelGGL(sort_count_kernel, dim3(a.n_ranges), dim3(64), lds, st, a.slot_expert, a.nslots,
+  hipLaunchKernelGGL((sort_count_kernel<LocalIds>), dim3(a.n_ranges), dim3(64), lds, st,
+                     LocalIds{a.slot_expert}, a.nslots,
                      a.Ep, a.n_ranges, a.range_counts);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
@@ -405,9 +422,50 @@ hipError_t launch_sort_and_gate(const SortArgs& a, hipStream_t st) {
                      a.counts, a.offsets, a.vinfo, a.units16, a.counters, a.dense_tiles);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.n_ranges), dim3(64), lds, st, a.slot_expert,
-                     a.nslots, a.Ep, a.n_ranges, key_bits, a.range_counts, a.offsets,
+  hipLaunchKernelGGL((sort_scatter_kernel<LocalIds>), dim3(a.n_ranges), dim3(64), lds, st,
+                     LocalIds{a.slot_expert}, a.nslots, a.Ep, a.n_ranges, key_bits, a.range_counts, a.offsets,
                      a.sorted_slot, a.expanded_idx);
+  return hipGetLastError();
+}
+
+// Expert offsets from the counts (one block): the dispatch operator's share of
+// sort_scan_kernel.
+__global__ __launch_bounds__(1024) void sort_offsets_kernel(int E,
+                                                            const int32_t* __restrict__ counts,
+                                                            int32_t* __restrict__ offsets) {
+  static_assert(kMaxExperts == 2048, "two experts a thread");
+  __shared__ int32_t s_w[16];
+  const int tid = threadIdx.x, w = tid >> 6;
+  const int a = 2 * tid < E ? counts[2 * tid] : 0, b = 2 * tid + 1 < E ? counts[2 * tid + 1] : 0;
+  const int incl = wave_incl_scan(a + b);
+  if (lane_id() == kWave - 1) s_w[w] = incl;
+  __syncthreads();
+  int at = incl - a - b;
+  for (int j = 0; j < w; ++j) at += s_w[j];
+  if (2 * tid < E) offsets[2 * tid] = at;
+  if (2 * tid + 1 < E) offsets[2 * tid + 1] = at + a;
+  if (tid == (E - 1) / 2) offsets[E] = at + a + b;
+}
+
+hipError_t launch_sort_maps(const SortMapsArgs& a, hipStream_t st) {
+  int key_bits = 1;
+  while ((1 << key_bits) <= a.E) ++key_bits;  // keys 0..E inclusive
+  const size_t lds = static_cast<size_t>(a.E) * sizeof(int32_t);
+  const GlobalIds ids{a.ids, a.expert_offset, a.E};
+  hipLaunchKernelGGL((sort_count_kernel<GlobalIds>), dim3(a.n_ranges), dim3(64), lds, st, ids,
+                     a.nslots, a.E, a.n_ranges, a.range_counts);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(sort_range_scan_kernel, dim3((a.E + kWave - 1) / kWave), dim3(256), 0, st,
+                     a.range_counts, a.n_ranges, a.E, a.counts);
+  err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(sort_offsets_kernel, dim3(1), dim3(1024), 0, st, a.E, a.counts, a.offsets);
+  err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((sort_scatter_kernel<GlobalIds>), dim3(a.n_ranges), dim3(64), lds, st, ids,
+                     a.nslots, a.E, a.n_ranges, key_bits, a.range_counts, a.offsets, a.sorted_slot,
+                     a.expanded_idx);
   return hipGetLastError();
 }
 
