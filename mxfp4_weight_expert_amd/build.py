@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_mxfp4.so")
 SOURCES = ["api.hip", "route.hip", "sort.hip", "quant.hip", "gemm.hip", "gemm_tiled.hip",
-           "finalize.hip", "pack.hip", "dispatch.hip", "combine.hip", "w4_linear.hip", "ops_api.hip"]
+           "finalize.hip", "pack.hip", "dispatch.hip", "combine.hip", "w4_bf16.hip", "w4_fp16.hip", "ops_api.hip"]
 ARCH = "gfx950"
 JOBS = 6  # sources compiled at once
 
