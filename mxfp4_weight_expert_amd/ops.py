@@ -11,7 +11,7 @@ import ctypes
 import functools
 from dataclasses import dataclass
 
-from . import MOE_OK, MoeError, _ptr, load_library
+from . import MOE_OK, MoeError, load_library
 
 __all__ = ["DispatchShape", "W4Shape", "dispatch_query", "dispatch", "dispatch_backward", "combine",
            "combine_backward", "w4_linear", "w4_grouped_linear", "DTYPE", "W4_FORMAT"]
@@ -31,6 +31,16 @@ class _W4Shape(ctypes.Structure):
                                                                ("ldo", ctypes.c_int64)]
 
 
+def _torch_dtype(name: str):
+    import torch
+
+    return getattr(torch, _TORCH_NAME[name])
+
+
+# A shape's C struct, torch types and array shapes are worked out at its first
+# call and kept on it: a decode step's calls are shorter than making them anew.
+
+
 @dataclass(frozen=True)
 class DispatchShape:
     """Shape of dispatch and combine (fields as in moe_ops_dispatch_shape)."""
@@ -45,6 +55,23 @@ class DispatchShape:
     def to_c(self) -> _DispatchShape:
         return _DispatchShape(self.T, self.E, self.topk, self.H, self.expert_offset,
                               DTYPE[self.dtype])
+
+    @functools.cached_property
+    def _c(self):
+        return ctypes.byref(self.to_c())
+
+    @functools.cached_property
+    def _torch(self):
+        return _torch_dtype(self.dtype)
+
+    @functools.cached_property
+    def _arrays(self):
+        """Shapes of tokens, rows and maps."""
+        return (self.T, self.H), (self.T * self.topk, self.H), (self.T, self.topk)
+
+    @functools.cached_property
+    def _workspace(self) -> int:
+        return dispatch_query(self)
 
 
 @dataclass(frozen=True)
@@ -65,38 +92,46 @@ class W4Shape:
         return _W4Shape(self.M, self.N, self.K, self.E, W4_FORMAT[self.format], self.group,
                         DTYPE[self.dtype], DTYPE[self.out_dtype or self.dtype], ldx, ldo)
 
+    @functools.cached_property
+    def _c(self):
+        return ctypes.byref(self.to_c())
+
+    @functools.cached_property
+    def _torch(self):
+        """Types of x, the scales and out."""
+        import torch
+
+        dt = _torch_dtype(self.dtype)
+        return dt, torch.uint8 if self.format == "mxfp4" else dt, _torch_dtype(self.out_dtype or self.dtype)
+
+    @functools.cached_property
+    def _arrays(self):
+        """Shapes of the codes, group values and bias of one matrix, and of all."""
+        if min(self.M, self.N - 1, self.K - 1, self.E - 1) < 0 or self.group < 1:
+            raise ValueError(f"sizes out of range: {self}")
+        one = ((self.N + 15) // 16 * 16, self.K // 2), (self.N, self.K // self.group), (self.N,)
+        return one, tuple((self.E, *s) for s in one)
+
 
 @functools.lru_cache(maxsize=None)
-def _lib():
-    lib = load_library()
+def _entry(name: str):
     vp, u64 = ctypes.c_void_p, ctypes.c_uint64
     ds, ws = ctypes.POINTER(_DispatchShape), ctypes.POINTER(_W4Shape)
-    for name, args in (
-            ("dispatch_query", [ds, ctypes.POINTER(u64)]),
-            ("dispatch", [vp, vp, ds, vp, vp, vp, vp, vp, u64, vp]),
-            ("dispatch_backward", [vp, vp, ds, vp, vp]),
-            ("combine", [vp, vp, vp, ds, vp, vp]),
-            ("combine_backward", [vp, vp, vp, vp, ds, vp, vp, vp]),
-            ("w4_linear", [vp, vp, vp, vp, vp, ws, vp, vp]),
-            ("w4_grouped_linear", [vp, vp, vp, vp, vp, vp, ws, vp, vp])):
-        fn = getattr(lib, "moe_ops_" + name)
-        fn.argtypes, fn.restype = args, ctypes.c_int
-    return lib
-
-
-@functools.lru_cache(maxsize=256)
-def _c_shape(shape, *strides):
-    return ctypes.byref(shape.to_c(*strides))
-
-
-def _torch_dtype(name: str):
-    import torch
-
-    return getattr(torch, _TORCH_NAME[name])
+    fn = getattr(load_library(), "moe_ops_" + name)
+    fn.argtypes = {
+        "dispatch_query": [ds, ctypes.POINTER(u64)],
+        "dispatch": [vp, vp, ds, vp, vp, vp, vp, vp, u64, vp],
+        "dispatch_backward": [vp, vp, ds, vp, vp],
+        "combine": [vp, vp, vp, ds, vp, vp],
+        "combine_backward": [vp, vp, vp, vp, ds, vp, vp, vp],
+        "w4_linear": [vp, vp, vp, vp, vp, ws, vp, vp],
+        "w4_grouped_linear": [vp, vp, vp, vp, vp, vp, ws, vp, vp]}[name]
+    fn.restype = ctypes.c_int
+    return fn
 
 
 def _check(t, what: str, shape: tuple, dtype, device):
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the first tensor on {device}")
@@ -104,19 +139,28 @@ def _check(t, what: str, shape: tuple, dtype, device):
         raise ValueError(f"{what} must be contiguous")
 
 
-def _rows_stride(t, what: str, shape: tuple, dtype, device) -> int:
-    """Elements between the rows of a matrix whose rows are contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+def _row_stride(t, what: str, shape: tuple, dtype, device) -> int:
+    """Elements between the rows of a matrix whose rows are contiguous; 0 where
+    the rows follow each other."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the first tensor on {device}")
-    if shape[0] <= 1:
-        if shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{what} must have contiguous rows")
+    if t.is_contiguous():
         return 0
-    if (shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < shape[1]:
+    if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
         raise ValueError(f"{what} must have contiguous rows that do not overlap")
-    return t.stride(0)
+    return t.stride(0) if shape[0] > 1 else 0
+
+
+def _result(t, what: str, shape: tuple, dtype, device):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        import torch
+
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, what, shape, dtype, device)
+    return t
 
 
 def _run(name: str, device, stream, *args):
@@ -125,14 +169,13 @@ def _run(name: str, device, stream, *args):
 
     if device.type != "cuda":
         raise ValueError(f"tensors must be on the GPU, got {device}")
-    fn = getattr(_lib(), "moe_ops_" + name)
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch._C._cuda_getDevice():
+        rc = _entry(name)(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = _entry(name)(*args, stream)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_ops_" + name)
 
@@ -140,7 +183,7 @@ def _run(name: str, device, stream, *args):
 def dispatch_query(shape: DispatchShape) -> int:
     """Workspace bytes of dispatch for a shape (raises MoeError if unsupported)."""
     n = ctypes.c_uint64()
-    rc = _lib().moe_ops_dispatch_query(_c_shape(shape), ctypes.byref(n))
+    rc = _entry("dispatch_query")(shape._c, ctypes.byref(n))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_ops_dispatch_query")
     return int(n.value)
@@ -158,33 +201,22 @@ def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_s
     """
     import torch
 
-    T, K, H, dev = shape.T, shape.topk, shape.H, x.device
-    dt, i32 = _torch_dtype(shape.dtype), torch.int32
-    nbytes = dispatch_query(shape)
-    _check(x, "x", (T, H), dt, dev)
-    _check(topk_ids, "topk_ids", (T, K), i32, dev)
-    if out is None:
-        out = torch.empty((T * K, H), dtype=dt, device=dev)
-    else:
-        _check(out, "out", (T * K, H), dt, dev)
-    if offsets is None:
-        offsets = torch.empty(shape.E + 1, dtype=i32, device=dev)
-    else:
-        _check(offsets, "offsets", (shape.E + 1,), i32, dev)
-    if row_slot is None:
-        row_slot = torch.empty(T * K, dtype=i32, device=dev)
-    else:
-        _check(row_slot, "row_slot", (T * K,), i32, dev)
-    if slot_row is None:
-        slot_row = torch.empty((T, K), dtype=i32, device=dev)
-    else:
-        _check(slot_row, "slot_row", (T, K), i32, dev)
+    dev, dt, i32 = x.device, shape._torch, torch.int32
+    nbytes = shape._workspace
+    tokens, sorted_rows, maps = shape._arrays
+    _check(x, "x", tokens, dt, dev)
+    _check(topk_ids, "topk_ids", maps, i32, dev)
+    out = _result(out, "out", sorted_rows, dt, dev)
+    offsets = _result(offsets, "offsets", (shape.E + 1,), i32, dev)
+    row_slot = _result(row_slot, "row_slot", sorted_rows[:1], i32, dev)
+    slot_row = _result(slot_row, "slot_row", maps, i32, dev)
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         _check(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    _run("dispatch", dev, stream, _ptr(x), _ptr(topk_ids), _c_shape(shape), _ptr(out),
-         _ptr(offsets), _ptr(row_slot), _ptr(slot_row), _ptr(workspace), workspace.numel())
+    _run("dispatch", dev, stream, x.data_ptr(), topk_ids.data_ptr(), shape._c, out.data_ptr(),
+         offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(), workspace.data_ptr(),
+         workspace.numel())
     return out, offsets, row_slot, slot_row
 
 
@@ -192,15 +224,13 @@ def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None, stream
     """Gradient of dispatch with respect to x: drows [T * topk, H] -> [T, H]."""
     import torch
 
-    T, K, H, dev = shape.T, shape.topk, shape.H, drows.device
-    dt = _torch_dtype(shape.dtype)
-    _check(drows, "drows", (T * K, H), dt, dev)
-    _check(slot_row, "slot_row", (T, K), torch.int32, dev)
-    if out is None:
-        out = torch.empty((T, H), dtype=dt, device=dev)
-    else:
-        _check(out, "out", (T, H), dt, dev)
-    _run("dispatch_backward", dev, stream, _ptr(drows), _ptr(slot_row), _c_shape(shape), _ptr(out))
+    dev, dt = drows.device, shape._torch
+    tokens, sorted_rows, maps = shape._arrays
+    _check(drows, "drows", sorted_rows, dt, dev)
+    _check(slot_row, "slot_row", maps, torch.int32, dev)
+    out = _result(out, "out", tokens, dt, dev)
+    _run("dispatch_backward", dev, stream, drows.data_ptr(), slot_row.data_ptr(), shape._c,
+         out.data_ptr())
     return out
 
 
@@ -211,17 +241,14 @@ def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None, stream=No
     """
     import torch
 
-    T, K, H, dev = shape.T, shape.topk, shape.H, rows.device
-    dt = _torch_dtype(shape.dtype)
-    _check(rows, "rows", (T * K, H), dt, dev)
-    _check(slot_row, "slot_row", (T, K), torch.int32, dev)
-    _check(topk_w, "topk_w", (T, K), torch.float32, dev)
-    if out is None:
-        out = torch.empty((T, H), dtype=dt, device=dev)
-    else:
-        _check(out, "out", (T, H), dt, dev)
-    _run("combine", dev, stream, _ptr(rows), _ptr(slot_row), _ptr(topk_w), _c_shape(shape),
-         _ptr(out))
+    dev, dt = rows.device, shape._torch
+    tokens, sorted_rows, maps = shape._arrays
+    _check(rows, "rows", sorted_rows, dt, dev)
+    _check(slot_row, "slot_row", maps, torch.int32, dev)
+    _check(topk_w, "topk_w", maps, torch.float32, dev)
+    out = _result(out, "out", tokens, dt, dev)
+    _run("combine", dev, stream, rows.data_ptr(), slot_row.data_ptr(), topk_w.data_ptr(), shape._c,
+         out.data_ptr())
     return out
 
 
@@ -232,56 +259,45 @@ def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=N
     weights without a row get 0."""
     import torch
 
-    T, K, H, dev = shape.T, shape.topk, shape.H, dout.device
-    dt = _torch_dtype(shape.dtype)
-    _check(dout, "dout", (T, H), dt, dev)
-    _check(rows, "rows", (T * K, H), dt, dev)
-    _check(slot_row, "slot_row", (T, K), torch.int32, dev)
-    _check(topk_w, "topk_w", (T, K), torch.float32, dev)
-    if dy is None:
-        dy = torch.empty((T * K, H), dtype=dt, device=dev)
-    else:
-        _check(dy, "dy", (T * K, H), dt, dev)
-    if dw is None:
-        dw = torch.empty((T, K), dtype=torch.float32, device=dev)
-    else:
-        _check(dw, "dw", (T, K), torch.float32, dev)
-    _run("combine_backward", dev, stream, _ptr(dout), _ptr(rows), _ptr(slot_row), _ptr(topk_w),
-         _c_shape(shape), _ptr(dy), _ptr(dw))
+    dev, dt = dout.device, shape._torch
+    tokens, sorted_rows, maps = shape._arrays
+    _check(dout, "dout", tokens, dt, dev)
+    _check(rows, "rows", sorted_rows, dt, dev)
+    _check(slot_row, "slot_row", maps, torch.int32, dev)
+    _check(topk_w, "topk_w", maps, torch.float32, dev)
+    dy = _result(dy, "dy", sorted_rows, dt, dev)
+    dw = _result(dw, "dw", maps, torch.float32, dev)
+    _run("combine_backward", dev, stream, dout.data_ptr(), rows.data_ptr(), slot_row.data_ptr(),
+         topk_w.data_ptr(), shape._c, dy.data_ptr(), dw.data_ptr())
     return dy, dw
 
 
 def _w4(name, x, offsets, w, scales, shape, zeros, bias, out, stream):
     import torch
 
-    M, N, K, E, dev = shape.M, shape.N, shape.K, shape.E, x.device
-    if min(M, N - 1, K - 1, E - 1) < 0 or shape.group < 1:
-        raise ValueError(f"sizes out of range: {shape}")
-    dt, groups = _torch_dtype(shape.dtype), K // shape.group
-    ldx = _rows_stride(x, "x", (M, K), dt, dev)
+    dev = x.device
+    dt, sdt, odt = shape._torch
+    one, every = shape._arrays
 
-    def matrix(t, what, tail, dtype):
-        bare = offsets is None and t.dim() == len(tail)  # one matrix, without its leading 1
-        _check(t, what, tail if bare else (E, *tail), dtype, dev)
+    def matrix(t, what, i, dtype):
+        if t is None:
+            return None
+        bare = offsets is None and t.dim() == len(one[i])  # one matrix, without its leading 1
+        _check(t, what, one[i] if bare else every[i], dtype, dev)
+        return t.data_ptr()
 
-    matrix(w, "w", ((N + 15) // 16 * 16, K // 2), torch.uint8)
-    matrix(scales, "scales", (N, groups), torch.uint8 if shape.format == "mxfp4" else dt)
-    if zeros is not None:
-        matrix(zeros, "zeros", (N, groups), torch.uint8)
-    if bias is not None:
-        matrix(bias, "bias", (N,), dt)
-    odt = _torch_dtype(shape.out_dtype or shape.dtype)
+    ldx, ldo = _row_stride(x, "x", (shape.M, shape.K), dt, dev), 0
     if out is None:
-        out = torch.empty((M, N), dtype=odt, device=dev)
-        ldo = 0
+        out = torch.empty((shape.M, shape.N), dtype=odt, device=dev)
     else:
-        ldo = _rows_stride(out, "out", (M, N), odt, dev)
-    args = [_ptr(x)]
+        ldo = _row_stride(out, "out", (shape.M, shape.N), odt, dev)
+    cshape = ctypes.byref(shape.to_c(ldx, ldo)) if ldx or ldo else shape._c
+    args = [matrix(w, "w", 0, torch.uint8), matrix(scales, "scales", 1, sdt),
+            matrix(zeros, "zeros", 1, torch.uint8), matrix(bias, "bias", 2, dt), cshape, out.data_ptr()]
     if offsets is not None:
-        _check(offsets, "offsets", (E + 1,), torch.int32, dev)
-        args.append(_ptr(offsets))
-    _run(name, dev, stream, *args, _ptr(w), _ptr(scales), _ptr(zeros), _ptr(bias),
-         _c_shape(shape, ldx, ldo), _ptr(out))
+        _check(offsets, "offsets", (shape.E + 1,), torch.int32, dev)
+        args.insert(0, offsets.data_ptr())
+    _run(name, dev, stream, x.data_ptr(), *args)
     return out
 
 

@@ -70,10 +70,10 @@ def test_dispatch_query_sizes():
     bad = _ds().to_c()
     bad.dtype = 3
     n = ctypes.c_uint64()
-    lib = ops._lib()
-    assert lib.moe_ops_dispatch_query(ctypes.byref(bad), ctypes.byref(n)) == 2
-    assert lib.moe_ops_dispatch_query(None, ctypes.byref(n)) == 1
-    assert lib.moe_ops_dispatch_query(ctypes.byref(_ds().to_c()), None) == 1
+    query = ops._entry("dispatch_query")
+    assert query(ctypes.byref(bad), ctypes.byref(n)) == 2
+    assert query(None, ctypes.byref(n)) == 1
+    assert query(ctypes.byref(_ds().to_c()), None) == 1
 
 
 MB = 1 << 20
@@ -88,7 +88,7 @@ def _p(v):
 
 def _dispatch(shape, wsb=1 << 30, **kw):
     a = {**A, **kw}
-    return ops._lib().moe_ops_dispatch(_p(a["x"]), _p(a["ids"]), ctypes.byref(shape.to_c()),
+    return ops._entry("dispatch")(_p(a["x"]), _p(a["ids"]), ctypes.byref(shape.to_c()),
                                        _p(a["rows"]), _p(a["offsets"]), _p(a["row_slot"]),
                                        _p(a["slot_row"]), _p(a["ws"]), wsb, None)
 
@@ -114,12 +114,12 @@ def test_dispatch_refuses_before_launch():
 
 def _combine(name, shape, **kw):
     a = {**A, **kw}
-    lib, sh = ops._lib(), ctypes.byref(shape.to_c())
+    sh = ctypes.byref(shape.to_c())
     if name == "dispatch_backward":
-        return lib.moe_ops_dispatch_backward(_p(a["rows"]), _p(a["slot_row"]), sh, _p(a["out"]), None)
+        return ops._entry("dispatch_backward")(_p(a["rows"]), _p(a["slot_row"]), sh, _p(a["out"]), None)
     if name == "combine":
-        return lib.moe_ops_combine(_p(a["rows"]), _p(a["slot_row"]), _p(a["w"]), sh, _p(a["out"]), None)
-    return lib.moe_ops_combine_backward(_p(a["x"]), _p(a["rows"]), _p(a["slot_row"]), _p(a["w"]), sh,
+        return ops._entry("combine")(_p(a["rows"]), _p(a["slot_row"]), _p(a["w"]), sh, _p(a["out"]), None)
+    return ops._entry("combine_backward")(_p(a["x"]), _p(a["rows"]), _p(a["slot_row"]), _p(a["w"]), sh,
                                         _p(a["out"]), _p(a["dw"]), None)
 
 
@@ -144,11 +144,11 @@ def _ws(**kw):
 
 def _w4(shape, grouped=False, ldx=0, ldo=0, **kw):
     a = {**A, "zeros": 0, "bias": 0, **kw}
-    lib, sh = ops._lib(), ctypes.byref(shape.to_c(ldx, ldo))
+    sh = ctypes.byref(shape.to_c(ldx, ldo))
     if grouped:
-        return lib.moe_ops_w4_grouped_linear(_p(a["x"]), _p(a["offsets"]), _p(a["w"]), _p(a["scales"]),
+        return ops._entry("w4_grouped_linear")(_p(a["x"]), _p(a["offsets"]), _p(a["w"]), _p(a["scales"]),
                                              _p(a["zeros"]), _p(a["bias"]), sh, _p(a["out"]), None)
-    return lib.moe_ops_w4_linear(_p(a["x"]), _p(a["w"]), _p(a["scales"]), _p(a["zeros"]),
+    return ops._entry("w4_linear")(_p(a["x"]), _p(a["w"]), _p(a["scales"]), _p(a["zeros"]),
                                  _p(a["bias"]), sh, _p(a["out"]), None)
 
 
@@ -184,9 +184,9 @@ def test_w4_refuses_before_launch():
     for field, v in (("format", 2), ("dtype", 3), ("out_dtype", 3), ("out_dtype", -1)):
         c = _ws().to_c()
         setattr(c, field, v)
-        assert ops._lib().moe_ops_w4_linear(_p(A["x"]), _p(A["w"]), _p(A["scales"]), None, None,
+        assert ops._entry("w4_linear")(_p(A["x"]), _p(A["w"]), _p(A["scales"]), None, None,
                                             ctypes.byref(c), _p(A["out"]), None) == 2, field
-    assert ops._lib().moe_ops_w4_linear(None, None, None, None, None, None, None, None) == 1
+    assert ops._entry("w4_linear")(None, None, None, None, None, None, None, None) == 1
 
 
 def test_binding_refuses_host_tensors_and_wrong_layouts():
