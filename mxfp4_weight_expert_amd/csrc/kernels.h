@@ -144,7 +144,7 @@ struct W4Args {
   int kw;  // waves of a block that split K (set by the launcher)
 };
 hipError_t launch_w4(const W4Args& a, hipStream_t st);
-hipError_t launch_w4_bf16(const W4Args& a, hipStream_t st);  // launch_w4's, with kw set
+hipError_t launch_w4_bf16(const W4Args& a, hipStream_t st);  // launch_w4's
 
 hipError_t launch_prepack(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t row_bytes,
                           hipStream_t st);

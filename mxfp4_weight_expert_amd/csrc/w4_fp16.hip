@@ -2,10 +2,7 @@
 #include "w4_kernel.h"
 
 namespace moe {
-hipError_t launch_w4(const W4Args& a0, hipStream_t st) {
-  W4Args a = a0;
-  // split K over the four waves from 8 steps on; below, each wave has weight rows of its own
-  a.kw = a.K >= 8 * 128 ? kW4Waves : 1;
+hipError_t launch_w4(const W4Args& a, hipStream_t st) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_w4_bf16(a, st) : w4_formats<MOE_DTYPE_FP16>(a, st);
 }
 }  // namespace moe

@@ -25,7 +25,9 @@
 #include "rows.h"
 #include "kernels.h"
 
+#include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace moe {
 
@@ -113,27 +115,25 @@ __device__ __forceinline__ constexpr int w4_layout(int fmt, int g, int dt) {
   return fmt == MOE_W4_MXFP4 ? (dt == MOE_DTYPE_BF16 ? kMix : kOne)
                              : (g == 32 ? kOne : g == 64 ? kHalf : kMix);
 }
-// Byte offset in a step's 256 bytes of a token row: quad q's 16 bytes for MFMA j.
+// The 16-byte piece (0..15) of a step's 256 bytes of a token row that quad q
+// feeds to MFMA j.
 template <int L>
-__device__ __forceinline__ constexpr uint32_t token_quad(uint32_t q) {
-  return L == kMix ? q * 64 : L == kHalf ? (q & 1) * 64 + (q >> 1) * 32 : q * 16;
-}
-template <int L>
-__device__ __forceinline__ constexpr uint32_t token_mfma(uint32_t j) {
-  return L == kMix ? j * 16 : L == kHalf ? (j & 1) * 16 + (j >> 1) * 128 : j * 64;
+__device__ __forceinline__ constexpr uint32_t token_piece(uint32_t q, uint32_t j) {
+  return L == kMix ? q * 4 + j
+                   : L == kHalf ? (q & 1) * 4 + (q >> 1) * 2 + (j & 1) + (j >> 1) * 8 : q + j * 4;
 }
 
-constexpr int kW4Waves = 4;
-// K steps in flight per wave: three where a step is 8 KB of tokens and weights,
-// two where the tokens alone are 8 or 16 KB.
-constexpr int w4_depth(int mt, int rb) { return mt == 1 ? (rb == 4 ? 3 : 4) : 2; }
+// K steps that a wave has in flight: 1 KB for each weight group and each four
+// rows of x. Three instead of two cost registers and gained nothing (64-token
+// decode of 896 experts: 145 against 143 us).
+constexpr int w4_depth(int mt) { return mt == 4 ? 1 : 2; }
 
-// One wave copies `bytes` (a multiple of ALIGN) of global memory to LDS with its
-// block: 16-byte pieces, then the last bytes one ALIGN unit a thread.
-template <int ALIGN>
+// The block copies `bytes` (a multiple of ALIGN) of global memory to LDS:
+// 16-byte pieces, then the last bytes one ALIGN unit a thread.
+template <int ALIGN, int W>
 __device__ __forceinline__ void block_to_lds(uint8_t* lds, const uint8_t* src, int bytes) {
   const int n = bytes >> 4, tid = threadIdx.x;
-  for (int c = tid; c < n; c += 256)
+  for (int c = tid; c < n; c += 64 * W)
     *reinterpret_cast<uint4*>(lds + 16 * c) = __builtin_bit_cast(
         uint4, static_cast<u32x4_t>(*reinterpret_cast<const u32x4_byte*>(src + 16 * c)));
   const int at = 16 * n + ALIGN * tid;
@@ -145,47 +145,60 @@ __device__ __forceinline__ void block_to_lds(uint8_t* lds, const uint8_t* src, i
   }
 }
 
-// LDS: the waves' parts, then the scale rows and the zero points of the block's
-// weight rows.
-template <int MT, int RB>
-__host__ __device__ constexpr int w4_part_bytes(int kw) { return kw == 1 ? 0 : kW4Waves * RB * MT * 1024; }
+// LDS: for each wave the token tile of a step (its parts of the sums at the
+// end), then the scale rows and the zero points of the block's weight rows.
+template <int MT, int W>
+__host__ __device__ constexpr int w4_token_bytes() { return W * MT * 4096; }
+
+// The same value, but not known to be: addresses made from it are worked out
+// where they are used. Hoisted out of the task loop, those of every unrolled
+// step, LDS read and store would hold some 70 registers a lane throughout.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // FMT, G: weight format and group; DT: tokens' type; MT: 16-row tiles of x a
 // task takes; RB: 16-row weight groups a wave takes.
 //
-// A task is a row tile times RB (kw = 4) or 4 RB (kw = 1) weight groups. With
-// kw = 4 the four waves split K and join in LDS at the end; with kw = 1 (short
-// K) each has weight groups of its own. A wave walks its K steps with a ring
-// of w4_depth steps in flight, tokens and weights; loads past its last step are
+// A task is a row tile times RB (kw = W) or W RB (kw = 1) weight groups. With
+// kw = W the block's waves split K and join in LDS at the end; with kw = 1 each
+// has weight groups of its own. A wave walks its K steps with a ring of
+// w4_depth steps in flight, tokens and weights; loads past its last step are
 // out of their buffer's range and touch no memory, so every step issues the
 // same loads and the waits cover the step being used alone. The scales of the
 // block's weight rows lie one after another and come to LDS in one copy.
-template <int FMT, int G, int DT, int MT, int RB>
-__global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
+//
+// What it costs beside the weights' stream, by leaving it out (64-token decode
+// of 896 experts, N 768, K 3584, when tokens came straight to the MFMA operands
+// with four loads a step): tokens 17 of 150 us, scales 8, decode and MFMAs
+// none; weights alone stream at 7.1 TB/s. Tokens loaded a KB at a time and
+// passed through LDS took 151 to 142 us.
+template <int FMT, int G, int DT, int MT, int RB, int W>
+__global__ __launch_bounds__(64 * W, W == 8 || MT == 2 ? 2 : MT == 1 ? 3 : 1) void w4_kernel(W4Args a) {
   constexpr int L = w4_layout(FMT, G, DT);
   constexpr bool kInt = FMT == MOE_W4_INT4;
   constexpr bool kFold = FMT == MOE_W4_MXFP4 && DT == MOE_DTYPE_BF16;  // scale in the convert
-  constexpr int D = w4_depth(MT, RB);
+  constexpr int D = w4_depth(MT);
   constexpr int kTile = 16 * MT;
   constexpr int kGroups = 128 / G;                   // groups of a step
   constexpr int kScale = kInt ? 2 : 1;               // bytes of a scale
   extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
   __shared__ int32_t s_first[kMaxExperts + 1];  // grouped: row tiles before each expert
-  __shared__ int32_t s_wave[kW4Waves];
+  __shared__ int32_t s_wave[W];
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_index();
-  const int r = lane & 15, q = lane >> 4;
   const int nk = a.K >> 7, ng = (a.N + 15) >> 4;
-  const int sets = kW4Waves / a.kw;  // sets of weight groups in the block
+  const int sets = W / a.kw;  // sets of weight groups in the block
   const int kpart = wv % a.kw, set = wv / a.kw;
   const int k0 = nk * kpart / a.kw, nsteps = nk * (kpart + 1) / a.kw - k0;
   const int ntn = (ng + RB * sets - 1) / (RB * sets);
   const int srow = nk * kGroups * kScale, zrow = nk * kGroups;  // bytes of a weight row's
-  uint8_t* const s_scale = s_dyn + w4_part_bytes<MT, RB>(a.kw);
+  uint8_t* const s_scale = s_dyn + w4_token_bytes<MT, W>();
   uint8_t* const s_zero = s_scale + ((RB * sets * 16 * srow + 15) & ~15);
 
   int tiles = (a.M + kTile - 1) / kTile;
   if (a.offsets != nullptr) {
-    constexpr int kPer = kMaxExperts / 256;
+    constexpr int kPer = kMaxExperts / (64 * W);
     int c[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -202,7 +215,7 @@ __global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
     __syncthreads();
     int at = incl - sum;
     tiles = 0;
-    for (int i = 0; i < kW4Waves; ++i) {
+    for (int i = 0; i < W; ++i) {
       if (i < wv) at += s_wave[i];
       tiles += s_wave[i];
     }
@@ -211,11 +224,15 @@ __global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
       s_first[tid * kPer + i] = at;
       at += c[i];
     }
-    if (tid == 255) s_first[kMaxExperts] = at;
+    if (tid == 64 * W - 1) s_first[kMaxExperts] = at;
     __syncthreads();
     tiles = __builtin_amdgcn_readfirstlane(tiles);
   }
   const int items = tiles * ntn;
+
+  const uint32_t xrow = static_cast<uint32_t>(a.ldx) * 2;
+  const uint32_t gbytes = static_cast<uint32_t>(nk) * kPkBlock;  // a weight group's
+  uint8_t* const s_tok = s_dyn + wv * MT * 4096;  // this wave's token tile
 
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     int e = 0, tn, row0, rows;
@@ -243,49 +260,26 @@ __global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
     }
     row0 = __builtin_amdgcn_readfirstlane(row0);
     rows = __builtin_amdgcn_readfirstlane(rows);
-    tn = __builtin_amdgcn_readfirstlane(tn);
-    const int bg0 = tn * RB * sets;       // the block's first weight group
-    const int rg0 = bg0 + set * RB;       // the wave's
-    const int live = min(RB, ng - rg0);   // groups of it that exist; may be <= 0
+    const int bg0 = __builtin_amdgcn_readfirstlane(tn) * RB * sets;  // the block's first weight group
+    const int rg0 = bg0 + set * RB;                                  // the wave's
 
-    // the block's scale rows; a task's first barrier is passed by a wave only
-    // after it has read the last one's
+    // The scales of the block's weight rows, in one contiguous copy. Every wave
+    // has passed the last task's barrier, and so has read the last of its scales.
     {
       const size_t row = static_cast<size_t>(e) * a.N + bg0 * 16;
       const int nrow = min(RB * sets * 16, a.N - bg0 * 16);
-      block_to_lds<kInt ? 2 : 4>(s_scale, static_cast<const uint8_t*>(a.scales) + row * srow, nrow * srow);
-      if (kInt && a.zeros != nullptr) block_to_lds<1>(s_zero, a.zeros + row * zrow, nrow * zrow);
+      block_to_lds<kInt ? 2 : 4, W>(s_scale, static_cast<const uint8_t*>(a.scales) + row * srow, nrow * srow);
+      if (kInt && a.zeros != nullptr) block_to_lds<1, W>(s_zero, a.zeros + row * zrow, nrow * zrow);
     }
 
-    // tokens: rows past the tile's are out of the buffer's range and read as 0
-    const uint32_t xrow = static_cast<uint32_t>(a.ldx) * 2;
+    // Rows past the tile's and weight groups past the last are out of the
+    // buffers' range: loads of them return 0 and touch no memory.
     const __amdgpu_buffer_rsrc_t xb = make_rsrc(
         static_cast<const uint8_t*>(a.x) + static_cast<size_t>(row0) * xrow,
         static_cast<uint32_t>(rows - 1) * xrow + static_cast<uint32_t>(a.K) * 2);
-    uint32_t xoff[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      xoff[t] = t * 16 + r < rows ? (t * 16 + r) * xrow + token_quad<L>(q) + k0 * 256 : kNoRow;
-    const uint32_t gbytes = static_cast<uint32_t>(nk) * kPkBlock;  // a weight group's
+    const int live = min(RB, ng - rg0);
     const __amdgpu_buffer_rsrc_t wb = make_rsrc(
         a.w + (static_cast<size_t>(e) * ng + rg0) * gbytes, live > 0 ? live * gbytes : 0);
-    const uint32_t woff = k0 * kPkBlock + r * 64 + q * 16;
-
-    uint4 xf[D][MT][4], w[D][RB];
-    auto load = [&](int d, int step) {  // step: wave-uniform
-      const bool in = step < nsteps;
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          xf[d][t][j] = bld16(xb, in ? xoff[t] + step * 256 + token_mfma<L>(j) : kNoRow);
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-        w[d][b] = bld16nt(wb, in ? woff + b * gbytes + step * kPkBlock : kNoRow);
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(d, d);
-    __syncthreads();  // scales are in LDS
 
     f32x4_t acc[RB][MT];
 #pragma unroll
@@ -293,87 +287,150 @@ __global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[b][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    auto compute = [&](int d, int ks) {
-      float xs[MT];  // lane (m, q): sum of row m's tokens of MFMA q
-      if constexpr (kInt) {
+    // The wave's K steps. XL: 1 KB loads of tokens a step, four rows each.
+    auto walk = [&](auto xlc) {
+      constexpr int XL = decltype(xlc)::value;
+      const int ln = opaque(lane), r = ln & 15, q = ln >> 4;
+      const uint32_t woff = k0 * kPkBlock + r * 64 + q * 16;
+      uint4 xg[D][XL], w[D][RB];
+      uint32_t xoff[XL], xlds[XL];
+#pragma unroll
+      for (int i = 0; i < XL; ++i) {
+        const uint32_t row = 4 * i + q;  // piece r of row 4 i + q
+        xoff[i] = row < static_cast<uint32_t>(rows) ? row * xrow + k0 * 256 + r * 16 : kNoRow;
+        xlds[i] = row * 256 + ((r ^ row) & 15) * 16;
+      }
+      // The blocks of an XCD take a row tile's steps from different places on:
+      // in step, all of them would ask one L2 channel for the same tokens, whose
+      // rows are often a multiple of the channels' span apart.
+      const int turn = ((item >> 3) + kpart * (nsteps >> 2)) % nsteps;
+      auto place = [&](int step) { return step + turn < nsteps ? step + turn : step + turn - nsteps; };
+      auto load = [&](int d, int step) {  // step: wave-uniform
+        const bool in = step < nsteps;
+        const int at = place(step);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) xg[d][i] = bld16(xb, in ? xoff[i] + at * 256 : kNoRow);
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+          w[d][b] = bld16nt(wb, in ? woff + b * gbytes + at * kPkBlock : kNoRow);
+      };
+#pragma unroll
+      for (int d = 0; d < D; ++d) load(d, d);
+      __syncthreads();  // scales are in LDS
+
+      auto compute = [&](int d, int ks) {
+        // Tokens through the wave's own LDS tile: loaded whole rows a KB at a
+        // time, read as the MFMAs want them. Piece c of row m lies at c ^ m, so
+        // the sixteen rows' pieces fall on different banks. Lanes of rows that
+        // were not loaded read one that was: their results are not stored.
+#pragma unroll
+        for (int i = 0; i < XL; ++i) *reinterpret_cast<uint4*>(s_tok + xlds[i]) = xg[d][i];
+        __builtin_amdgcn_wave_barrier();
+        uint4 xf[MT][4];
+        float xs[MT];  // lane (m, q): of the sum of row m's tokens, INT4
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t m = XL < 4 ? r & (4 * XL - 1) : t * 16 + r;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t one = r == 4 * j ? (DT == MOE_DTYPE_BF16 ? 0x3f803f80u : 0x3c003c00u) : 0u;
-            sum = mfma_rows<DT>(uint4{one, one, one, one}, xf[d][t][j], sum);
-            xf[d][t][j] = even_odd(xf[d][t][j]);
+          for (int j = 0; j < 4; ++j)
+            xf[t][j] = *reinterpret_cast<const uint4*>(
+                s_tok + m * 256 + ((token_piece<L>(q, j) ^ m) & 15) * 16);
+          if constexpr (kInt) {
+            // MFMAs with ones for weights: every lane (m, q) gets row m's sum of
+            // each group, and keeps its share of the one that its scales belong to
+            const uint32_t one = DT == MOE_DTYPE_BF16 ? 0x3f803f80u : 0x3c003c00u;
+            constexpr int kPer = 4 / kGroups;
+            f32x4_t sum[kGroups];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (j % kPer == 0) sum[j / kPer] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+              sum[j / kPer] = mfma_rows<DT>(uint4{one, one, one, one}, xf[t][j], sum[j / kPer]);
+              xf[t][j] = even_odd(xf[t][j]);
+            }
+            xs[t] = sum[0][0];
+#pragma unroll
+            for (int g = 1; g < kGroups; ++g) xs[t] = q / kPer == g ? sum[g][0] : xs[t];
+            xs[t] *= 1.0f / kPer;  // the group's kPer lanes add up to it
           }
-          xs[t] = sum[0];
         }
-      }
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const int wr = (set * RB + b) * 16 + r;  // weight row in the block's
-        uint32_t dw[4] = {w[d][b].x, w[d][b].y, w[d][b].z, w[d][b].w};
-        if constexpr (kFold) {
-          const float s = e8m0_scale_operand(s_scale[wr * srow + ks * 4 + q]);
+        for (int b = 0; b < RB; ++b) {
+          const int wr = (set * RB + b) * 16 + r;  // weight row in the block's
+          uint32_t dw[4] = {w[d][b].x, w[d][b].y, w[d][b].z, w[d][b].w};
+          if constexpr (kFold) {
+            const float s = e8m0_scale_operand(s_scale[wr * srow + ks * 4 + q]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint4 f = __builtin_bit_cast(uint4, decode_fp4x8(dw[j], s));
+            for (int j = 0; j < 4; ++j) {
+              const uint4 f = __builtin_bit_cast(uint4, decode_fp4x8(dw[j], s));
 #pragma unroll
-            for (int t = 0; t < MT; ++t) acc[b][t] = mfma_rows<DT>(xf[d][t][j], f, acc[b][t]);
-          }
-        } else {
-          constexpr int kPer = 4 / kGroups;  // MFMAs a group's sum takes
-          float s[kGroups];
-          const uint8_t* sp = s_scale + wr * srow + ks * kGroups * kScale;
-          if constexpr (!kInt) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(sp);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) s[g] = e8m0_value((v >> (8 * g)) & 0xffu);
+              for (int t = 0; t < MT; ++t) acc[b][t] = mfma_rows<DT>(xf[t][j], f, acc[b][t]);
+            }
           } else {
+            constexpr int kPer = 4 / kGroups;  // MFMAs a group's sum takes
+            float s[kGroups];
+            const uint8_t* sp = s_scale + wr * srow + ks * kGroups * kScale;
+            if constexpr (!kInt) {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(sp);
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-              s[g] = scale16<DT>(reinterpret_cast<const uint16_t*>(sp)[g]);
-          }
-          if constexpr (L == kOne) {
-            transpose_quads(dw);
-          } else if constexpr (L == kHalf) {
-            swap32(dw[0], dw[2]);
-            swap32(dw[1], dw[3]);
-          }
-          f32x4_t part[MT];
+              for (int g = 0; g < kGroups; ++g) s[g] = e8m0_value((v >> (8 * g)) & 0xffu);
+            } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 f;
-            if constexpr (kInt) f = decode_int4x8<DT>(dw[j]);
-            else f = decode_fp4x8_f16(dw[j]);
+              for (int g = 0; g < kGroups; ++g)
+                s[g] = scale16<DT>(reinterpret_cast<const uint16_t*>(sp)[g]);
+            }
+            if constexpr (L == kOne) {
+              transpose_quads(dw);
+            } else if constexpr (L == kHalf) {
+              swap32(dw[0], dw[2]);
+              swap32(dw[1], dw[3]);
+            }
+            f32x4_t part[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              if (j % kPer == 0) part[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-              part[t] = mfma_rows<DT>(xf[d][t][j], f, part[t]);
-              if (j % kPer == kPer - 1) {
+            for (int j = 0; j < 4; ++j) {
+              uint4 f;
+              if constexpr (kInt) f = decode_int4x8<DT>(dw[j]);
+              else f = decode_fp4x8_f16(dw[j]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[b][t][i] += s[j / kPer] * part[t][i];
+              for (int t = 0; t < MT; ++t) {
+                if (j % kPer == 0) part[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                part[t] = mfma_rows<DT>(xf[t][j], f, part[t]);
+                if (j % kPer == kPer - 1) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) acc[b][t][i] += s[j / kPer] * part[t][i];
+                }
               }
             }
-          }
-          if constexpr (kInt) {
-            const int gq = q / kPer;
-            float z = 8.0f, sq = s[0];
-            if (a.zeros != nullptr) z = static_cast<float>(s_zero[wr * zrow + ks * kGroups + gq]);
+            if constexpr (kInt) {
+              const int gq = q / kPer;
+              float z = 8.0f, sq = s[0];
+              if (a.zeros != nullptr) z = static_cast<float>(s_zero[wr * zrow + ks * kGroups + gq]);
 #pragma unroll
-            for (int g = 1; g < kGroups; ++g) sq = gq == g ? s[g] : sq;
+              for (int g = 1; g < kGroups; ++g) sq = gq == g ? s[g] : sq;
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-              acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xs[t], -sq * z, acc[b][t], 0, 0, 0);
+              for (int t = 0; t < MT; ++t)
+                acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xs[t], -sq * z, acc[b][t], 0, 0, 0);
+            }
           }
+          __builtin_amdgcn_sched_barrier(0);  // one weight group's decode at a time: registers
+        }
+      };
+      for (int s0 = 0; s0 < nsteps; s0 += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (s0 + d < nsteps) compute(d, k0 + place(s0 + d));
+          __builtin_amdgcn_sched_barrier(0);
+          load(d, s0 + d + D);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     };
-    for (int s0 = 0; s0 < nsteps; s0 += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (s0 + d < nsteps) compute(d, k0 + s0 + d);
-        load(d, s0 + d + D);
-      }
+    if constexpr (MT > 1) {
+      walk(std::integral_constant<int, 4 * MT>{});
+    } else {
+      if (rows <= 4) walk(std::integral_constant<int, 1>{});
+      else if (rows <= 8) walk(std::integral_constant<int, 2>{});
+      else walk(std::integral_constant<int, 4>{});
     }
 
     // Join the waves that share weight rows, and store: value (m, n) of a tile
@@ -388,6 +445,7 @@ __global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
       else static_cast<_Float16*>(a.out)[at] = static_cast<_Float16>(v);
     };
     if (a.kw == 1) {
+      const int ln = opaque(lane), r = ln & 15, q = ln >> 4;
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
@@ -396,36 +454,37 @@ __global__ __launch_bounds__(256) void w4_kernel(W4Args a) {
           for (int i = 0; i < 4; ++i) store(t * 16 + q * 4 + i, (rg0 + b) * 16 + r, acc[b][t][i]);
       __syncthreads();  // before the next task's scales
     } else {
-      f32x4_t* part = reinterpret_cast<f32x4_t*>(s_dyn);  // [wave][RB * MT][lane]
+      // in place of the wave's tokens: [RB * MT][lane] of MT * 256 places
+      static_assert(RB <= 4, "a wave's sums fit its token tile");
+      f32x4_t* part = reinterpret_cast<f32x4_t*>(s_dyn);
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) part[(wv * RB * MT + b * MT + t) * kWave + lane] = acc[b][t];
+        for (int t = 0; t < MT; ++t) part[(wv * 4 * MT + b * MT + t) * kWave + opaque(lane)] = acc[b][t];
       __syncthreads();
-      const int m = tid >> 4, nn = tid & 15;
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+      for (int i = 0; i < RB * MT * 256; i += 64 * W) {
+        const int at = i + opaque(tid), bt = at >> 8, m = (at >> 4) & 15, nn = at & 15;
+        if (RB * MT * 256 % (64 * W) != 0 && at >= RB * MT * 256) break;
+        float v = 0.0f;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          float v = 0.0f;
-#pragma unroll
-          for (int u = 0; u < kW4Waves; ++u)
-            v += reinterpret_cast<const float*>(
-                part + (u * RB * MT + b * MT + t) * kWave + (m >> 2) * 16 + nn)[m & 3];
-          store(t * 16 + m, (rg0 + b) * 16 + nn, v);
-        }
+        for (int u = 0; u < W; ++u)
+          v += reinterpret_cast<const float*>(
+              part + (u * 4 * MT + bt) * kWave + (m >> 2) * 16 + nn)[m & 3];
+        store(bt % MT * 16 + m, (rg0 + bt / MT) * 16 + nn, v);
+      }
     }
   }
 }
 
 // Blocks of a kernel that a CU holds, by its LDS (kept per size and instance).
 template <class F>
-int w4_resident(F kernel, int lds) {
+int w4_resident(F kernel, int threads, int lds) {
   static std::atomic<int> kept[161];
   std::atomic<int>& k = kept[lds >> 10];
   int n = k.load(std::memory_order_relaxed);
   if (n == 0) {
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(kernel), 256,
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(kernel), threads,
                                                      (lds | 1023) + 1) != hipSuccess || n < 1)
       n = 1;
     k.store(n, std::memory_order_relaxed);
@@ -433,39 +492,68 @@ int w4_resident(F kernel, int lds) {
   return n;
 }
 
-template <int FMT, int G, int DT, int MT, int RB>
+template <int FMT, int G, int DT, int MT, int RB, int W>
 void w4_go(const W4Args& a, hipStream_t st) {
   constexpr bool kInt = FMT == MOE_W4_INT4;
-  const int64_t sets = kW4Waves / a.kw;
+  const int64_t sets = W / a.kw;
   const int64_t ntn = ((a.N + 15) / 16 + RB * sets - 1) / (RB * sets);
   const int64_t tiles = (a.M + 16 * MT - 1) / (16 * MT) + (a.offsets != nullptr ? a.E : 0);
   const int64_t items = ntn * tiles;
   const int groups = (a.K >> 7) * (128 / G), nrow = RB * static_cast<int>(sets) * 16;
-  const int lds = w4_part_bytes<MT, RB>(a.kw) + ((nrow * groups * (kInt ? 2 : 1) + 15) & ~15) +
+  const int lds = w4_token_bytes<MT, W>() + ((nrow * groups * (kInt ? 2 : 1) + 15) & ~15) +
                   (kInt && a.zeros != nullptr ? (nrow * groups + 15) & ~15 : 0);
-  auto kernel = w4_kernel<FMT, G, DT, MT, RB>;
-  const int64_t most = int64_t{256} * w4_resident(kernel, lds);
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(256), lds,
+  auto kernel = w4_kernel<FMT, G, DT, MT, RB, W>;
+  const int64_t most = int64_t{256} * w4_resident(kernel, 64 * W, lds);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(64 * W), lds,
                      st, a);
 }
 
+// The variant of a shape. U is the number of 16-row weight groups that can be
+// read (an expert without rows reads none), nk the K steps.
+//
+// - Many groups (U >= 2048): RB = 4, whose loads of tokens serve four groups.
+//   kw = 1 reads a group's whole K in one wave, with no join, but takes tasks four
+//   times as long: chosen where rounds of resident blocks times (steps + 4), the 4
+//   for a task's start and end, come out lower. K 384 x N 3584 of 896 experts:
+//   98 us against 204 with kw = 4; K 7168 x N 4096 of 64 experts: 166 against 135.
+// - Fewer: RB = 2, or 1 up to a group a CU, and K over eight waves from 16 steps on.
+//   8192 x 8192, 1 and 16 tokens: 9.3 and 12.3 us with RB = 2 and eight waves, 9.7
+//   and 15.3 with RB = 1, 13.4 and 15.6 with RB = 4 and four waves. 4096 x 4096:
+//   5.6 and 7.2, 4.8 and 6.1, 8.4 and 9.7. 24576 x 2048, one token: 7.2 with RB = 2
+//   and four waves, 8.8 with RB = 4.
+// Row tiles (MT) go by the rows an expert has on average.
+constexpr int kW4Kw1Scales = 36 << 10;  // with 16 KB of tokens, three blocks in a CU's LDS
 template <int FMT, int G, int DT>
-void w4_rows(const W4Args& a, hipStream_t st) {
-  // tiles of x rows: by the rows an expert has on average
-  const int per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;
-  // weight groups a wave takes: as many as leave two tasks for every CU
-  const int64_t groups = static_cast<int64_t>((a.N + 15) / 16) * (a.offsets != nullptr ? a.E : 1);
-  const int64_t tasks = groups * a.kw / kW4Waves;
-  if (per <= 16) {
-    if (tasks >= 4 * 512) w4_go<FMT, G, DT, 1, 4>(a, st);
-    else if (tasks >= 2 * 256) w4_go<FMT, G, DT, 1, 2>(a, st);
-    else w4_go<FMT, G, DT, 1, 1>(a, st);
-  } else if (per <= 32) {
-    if (tasks >= 4 * 256) w4_go<FMT, G, DT, 2, 4>(a, st);
-    else w4_go<FMT, G, DT, 2, 1>(a, st);
+void w4_rows(const W4Args& a0, hipStream_t st) {
+  W4Args a = a0;
+  const bool grouped = a.offsets != nullptr;
+  const int per = grouped ? (a.M + a.E - 1) / a.E : a.M;
+  const int64_t U = static_cast<int64_t>((a.N + 15) / 16) * (grouped ? std::min(a.E, a.M) : 1);
+  const int nk = a.K >> 7;
+  a.kw = 4;
+  // scale rows (and zero points) of a kw = 1 block's RB * 64 weight rows in LDS
+  const int scales = (per > 16 ? 128 : 256) * nk * (128 / G) *
+                     (a.format == MOE_W4_MXFP4 ? 1 : a.zeros != nullptr ? 3 : 2);
+  if (U >= 2048 && scales <= kW4Kw1Scales) {
+    constexpr int64_t kBlocks = 256 * 3;  // resident, as a rule
+    const auto cost = [&](int64_t tasks, int steps) { return (tasks + kBlocks - 1) / kBlocks * (steps + 4); };
+    if (cost(U / 16, nk) <= cost(U / 4, (nk + 3) / 4)) a.kw = 1;
+  }
+  if (per > 32) {
+    if (U >= 512) w4_go<FMT, G, DT, 4, 2, 4>(a, st);
+    else w4_go<FMT, G, DT, 4, 1, 4>(a, st);
+  } else if (per > 16) {
+    if (U >= 512) w4_go<FMT, G, DT, 2, 2, 4>(a, st);
+    else w4_go<FMT, G, DT, 2, 1, 4>(a, st);
+  } else if (U >= 2048) {
+    w4_go<FMT, G, DT, 1, 4, 4>(a, st);
+  } else if (U > 512 || nk < 16) {
+    if (U > 256) w4_go<FMT, G, DT, 1, 2, 4>(a, st);
+    else w4_go<FMT, G, DT, 1, 1, 4>(a, st);
   } else {
-    if (tasks >= 2 * 256) w4_go<FMT, G, DT, 4, 2>(a, st);
-    else w4_go<FMT, G, DT, 4, 1>(a, st);
+    a.kw = 8;
+    if (U > 256) w4_go<FMT, G, DT, 1, 2, 8>(a, st);
+    else w4_go<FMT, G, DT, 1, 1, 8>(a, st);
   }
 }
 

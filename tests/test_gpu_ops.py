@@ -268,6 +268,15 @@ LINEAR = [
     (5, 1000, 8192, "mxfp4", 32, "bf16", "fp32", False, False),
     (7, 5000, 128, "mxfp4", 32, "bf16", "bf16", False, False),
     (1, 7168, 2048, "mxfp4", 32, "bf16", "bf16", False, False),
+    # many weight groups: four to a wave, K split over the waves, or not (short K)
+    (3, 32900, 1024, "mxfp4", 32, "bf16", "bf16", False, True),
+    (16, 32770, 1152, "int4", 32, "bf16", "fp32", True, False),
+    (6, 200000, 128, "int4", 64, "fp16", "fp16", True, False),
+    (20, 40001, 256, "int4", 128, "bf16", "bf16", False, False),
+    (50, 40001, 256, "mxfp4", 32, "fp16", "fp32", False, False),
+    # K over eight waves
+    (9, 5000, 2176, "int4", 64, "bf16", "fp32", False, True),
+    (12, 40, 7168, "int4", 32, "fp16", "fp32", True, False),
 ]
 
 
@@ -367,6 +376,9 @@ GROUPED = [
     ([2] * 100, 700, 20, 384, "mxfp4", 32, "fp16", "fp32", False, False),
     ([33, 34, 31, 0, 90], 0, 100, 1536, "mxfp4", 32, "bf16", "bf16", False, False),
     ([5, 1, 0, 3], 100, 768, 3584, "mxfp4", 32, "bf16", "fp32", False, False),
+    # one wave a weight group's K, and zero points and scales that would not fit LDS then
+    ([1, 0, 3, 5, 9, 2] * 20, 3, 500, 384, "int4", 32, "bf16", "fp32", True, True),
+    ([2, 1] * 8, 0, 4096, 8192, "int4", 32, "fp16", "fp32", True, False),
 ]
 
 
