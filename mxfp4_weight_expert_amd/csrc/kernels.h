@@ -90,17 +90,17 @@ struct FinalizeArgs {
 };
 hipError_t launch_finalize(const FinalizeArgs& a, hipStream_t st);
 
-// Maps of the dispatch operator from global ids: the sort's kernels for many
-// slots, without the layer's chunk tables and gate.
+// Maps of the dispatch operator from global ids, for many slots (sort.hip).
 struct SortMapsArgs {
   const int32_t* ids;  // [nslots] global ids
-  int nslots, E, expert_offset, n_ranges;
-  int32_t* range_counts;  // [n_ranges, E]
+  int nslots, E, expert_offset;
+  int32_t* range_counts;  // [ranges of map_range_slots(nslots) slots, E]
   int32_t* counts;        // [E]
   int32_t* offsets;       // [E + 1]
-  int32_t* sorted_slot;   // [nslots]
-  int32_t* expanded_idx;  // [nslots]
+  int32_t* row_slot;      // [nslots]
+  int32_t* slot_row;      // [nslots]
 };
+int map_range_slots(int64_t nslots);
 hipError_t launch_sort_maps(const SortMapsArgs& a, hipStream_t st);
 
 // Slots up to which dispatch is one launch (dispatch.hip).

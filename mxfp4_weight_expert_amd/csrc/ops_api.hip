@@ -41,7 +41,8 @@ struct DispatchWs {
 DispatchWs dispatch_ws(const moe_ops_dispatch_shape& s) {
   const uint64_t slots = static_cast<uint64_t>(s.T) * s.topk;
   if (slots <= static_cast<uint64_t>(kFusedSlots)) return {0, 256};
-  const uint64_t ranges = (slots + kRangeSlots - 1) / kRangeSlots;
+  const uint64_t len = map_range_slots(static_cast<int64_t>(slots));
+  const uint64_t ranges = (slots + len - 1) / len;
   const uint64_t counts = (ranges * s.E * 4 + 255) / 256 * 256;
   return {counts, counts + (static_cast<uint64_t>(s.E) * 4 + 255) / 256 * 256};
 }

@@ -262,25 +262,10 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(
 }
 
 // ------------------------------------------------------------ large shapes
-// Where the range kernels read a slot's expert: the layer's local ids as they
-// are, or global ids (dispatch), whose local id is -1 outside the range.
-struct LocalIds {
-  const int32_t* ids;
-  __device__ __forceinline__ int operator()(int s) const { return ids[s]; }
-};
-struct GlobalIds {
-  const int32_t* ids;
-  int offset, E;
-  __device__ __forceinline__ int operator()(int s) const {
-    const int id = ids[s];
-    return id >= offset && id - offset < E ? id - offset : -1;
-  }
-};
-
 // One wave per block (ranges spread over the CUs): range r's expert
 // histogram in LDS, written range-major to range_counts[r][Ep].
-template <class Ids>
-__global__ __launch_bounds__(64) void sort_count_kernel(const Ids slot_expert, int nslots, int Ep, int n_ranges,
+__global__ __launch_bounds__(64) void sort_count_kernel(const int32_t* __restrict__ slot_expert,
+                                                        int nslots, int Ep, int n_ranges,
                                                         int32_t* __restrict__ range_counts) {
   extern __shared__ int32_t lds[];
   const int lane = lane_id();
@@ -291,7 +276,7 @@ __global__ __launch_bounds__(64) void sort_count_kernel(const Ids slot_expert, i
   const int s0 = r * kRangeSlots;
   const int s1 = min(nslots, s0 + kRangeSlots);
   for (int s = s0 + lane; s < s1; s += kWave) {
-    const int e = slot_expert(s);
+    const int e = slot_expert[s];
     if (e >= 0) atomicAdd(&h[e], 1);
   }
   __builtin_amdgcn_wave_barrier();
@@ -370,9 +355,8 @@ __global__ __launch_bounds__(1024) void sort_scan_kernel(int Ep, int B, int forc
                       dense_tiles, nullptr);
 }
 
-template <class Ids>
 __global__ __launch_bounds__(64) void sort_scatter_kernel(
-    const Ids slot_expert, int nslots, int Ep, int n_ranges, int key_bits,
+    const int32_t* __restrict__ slot_expert, int nslots, int Ep, int n_ranges, int key_bits,
     const int32_t* __restrict__ range_base, const int32_t* __restrict__ offsets,
     int32_t* __restrict__ sorted_slot, int32_t* __restrict__ expanded_idx) {
   constexpr int kGroups = kRangeSlots / kWave;
@@ -384,7 +368,7 @@ __global__ __launch_bounds__(64) void sort_scatter_kernel(
   // the range's experts, all loads in flight at once (clamped index)
   int ex[kGroups];
 #pragma unroll
-  for (int gi = 0; gi < kGroups; ++gi) ex[gi] = slot_expert(min(s0 + gi * kWave + lane, nslots - 1));
+  for (int gi = 0; gi < kGroups; ++gi) ex[gi] = slot_expert[min(s0 + gi * kWave + lane, nslots - 1)];
   int32_t* next = lds;  // next free row per expert for this range
   for (int i = lane; i < Ep; i += kWave)
     next[i] = offsets[i] + range_base[static_cast<size_t>(r) * Ep + i];
@@ -409,8 +393,7 @@ hipError_t launch_sort_and_gate(const SortArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   const size_t lds = static_cast<size_t>(a.Ep) * sizeof(int32_t);
-  hipLaunchKernelGGL((sort_count_kernel<LocalIds>), dim3(a.n_ranges), dim3(64), lds, st,
-                     LocalIds{a.slot_expert}, a.nslots,
+  hipLaunchKernelGGL(sort_count_kernel, dim3(a.n_ranges), dim3(64), lds, st, a.slot_expert, a.nslots,
                      a.Ep, a.n_ranges, a.range_counts);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
@@ -422,51 +405,160 @@ hipError_t launch_sort_and_gate(const SortArgs& a, hipStream_t st) {
                      a.counts, a.offsets, a.vinfo, a.units16, a.counters, a.dense_tiles);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((sort_scatter_kernel<LocalIds>), dim3(a.n_ranges), dim3(64), lds, st,
-                     LocalIds{a.slot_expert}, a.nslots, a.Ep, a.n_ranges, key_bits, a.range_counts, a.offsets,
+  hipLaunchKernelGGL(sort_scatter_kernel, dim3(a.n_ranges), dim3(64), lds, st, a.slot_expert,
+                     a.nslots, a.Ep, a.n_ranges, key_bits, a.range_counts, a.offsets,
                      a.sorted_slot, a.expanded_idx);
   return hipGetLastError();
 }
 
-// Expert offsets from the counts (one block): the dispatch operator's share of
-// sort_scan_kernel.
-__global__ __launch_bounds__(1024) void sort_offsets_kernel(int E,
-                                                            const int32_t* __restrict__ counts,
-                                                            int32_t* __restrict__ offsets) {
-  static_assert(kMaxExperts == 2048, "two experts a thread");
-  __shared__ int32_t s_w[16];
-  const int tid = threadIdx.x, w = tid >> 6;
-  const int a = 2 * tid < E ? counts[2 * tid] : 0, b = 2 * tid + 1 < E ? counts[2 * tid + 1] : 0;
-  const int incl = wave_incl_scan(a + b);
-  if (lane_id() == kWave - 1) s_w[w] = incl;
-  __syncthreads();
-  int at = incl - a - b;
-  for (int j = 0; j < w; ++j) at += s_w[j];
-  if (2 * tid < E) offsets[2 * tid] = at;
-  if (2 * tid + 1 < E) offsets[2 * tid + 1] = at + a;
-  if (tid == (E - 1) / 2) offsets[E] = at + a + b;
+// ------------------------------------------------------------ dispatch maps
+// The dispatch operator's sort: the range scheme above on global ids (those
+// outside [offset, offset + E) have no row), without chunk tables and gate, in
+// three launches. Shorter ranges than the layer's while the range scan is small:
+// at 131k slots and 896 experts on MI355X count, scan and placement took 11, 5
+// and 15 us with ranges of 1024, all loads of a range one after another and the
+// expert offsets in a launch of their own (2 to 5 us).
+constexpr int kMapWaves = 16;
+constexpr int kShortRange = 256, kShortRangeSlots = 1 << 18;
+
+int map_range_slots(int64_t nslots) { return nslots <= kShortRangeSlots ? kShortRange : kRangeSlots; }
+
+// The experts of a one-wave range, -1 without a row or past the range's end,
+// all loads in flight at once.
+template <int N>
+__device__ __forceinline__ void load_range(const int32_t* ids, int s0, int s1, int offset, int E,
+                                           int (&ex)[N]) {
+#pragma unroll
+  for (int g = 0; g < N; ++g) ex[g] = ids[min(s0 + g * kWave + lane_id(), s1 - 1)];
+#pragma unroll
+  for (int g = 0; g < N; ++g) {
+    const bool here = s0 + g * kWave + lane_id() < s1 && ex[g] >= offset && ex[g] - offset < E;
+    ex[g] = here ? ex[g] - offset : -1;
+  }
 }
 
-hipError_t launch_sort_maps(const SortMapsArgs& a, hipStream_t st) {
+template <int SLOTS>
+__global__ __launch_bounds__(64) void map_count_kernel(const int32_t* __restrict__ ids, int nslots,
+                                                       int offset, int E,
+                                                       int32_t* __restrict__ range_counts) {
+  extern __shared__ int32_t lds[];
+  const int s0 = blockIdx.x * SLOTS;
+  int ex[SLOTS / kWave];
+  load_range(ids, s0, min(nslots, s0 + SLOTS), offset, E, ex);
+  for (int i = lane_id(); i < E; i += kWave) lds[i] = 0;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int g = 0; g < SLOTS / kWave; ++g)
+    if (ex[g] >= 0) atomicAdd(&lds[ex[g]], 1);  // whole numbers: the order changes nothing
+  __builtin_amdgcn_wave_barrier();
+  int32_t* out = range_counts + static_cast<size_t>(blockIdx.x) * E;
+  for (int i = lane_id(); i < E; i += kWave) out[i] = lds[i];
+}
+
+// Per expert, the exclusive scan of its counts over the ranges, in place, and
+// their total. A block takes 64 experts, one a lane, and its waves a part of the
+// ranges each, kMapLoads at a time; a part of one load keeps it in registers.
+constexpr int kMapLoads = 32;
+__global__ __launch_bounds__(64 * kMapWaves) void map_scan_kernel(
+    int32_t* __restrict__ range_counts, int n_ranges, int E, int32_t* __restrict__ counts) {
+  __shared__ int32_t s_part[kMapWaves][kWave];
+  const int lane = lane_id(), w = wave_index();
+  const int e = blockIdx.x * kWave + lane, ec = min(e, E - 1);
+  const int per = (n_ranges + kMapWaves - 1) / kMapWaves;
+  const int lo = min(w * per, n_ranges), hi = min(lo + per, n_ranges);
+  int32_t* const col = range_counts + ec;
+  int c[kMapLoads], sum = 0;
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int j = 0; j < kMapLoads; ++j)
+      c[j] = r0 + j < hi ? col[static_cast<size_t>(r0 + j) * E] : 0;
+  };
+  for (int r0 = lo; r0 < hi; r0 += kMapLoads) {
+    load(r0);
+#pragma unroll
+    for (int j = 0; j < kMapLoads; ++j) sum += c[j];
+  }
+  s_part[w][lane] = sum;
+  __syncthreads();
+  int run = 0;
+  for (int i = 0; i < w; ++i) run += s_part[i][lane];
+  if (e >= E) return;  // no barrier follows
+  if (w == kMapWaves - 1) counts[e] = run + sum;
+  for (int r0 = lo; r0 < hi; r0 += kMapLoads) {
+    if (hi - lo > kMapLoads) load(r0);
+#pragma unroll
+    for (int j = 0; j < kMapLoads; ++j) {
+      if (r0 + j < hi) col[static_cast<size_t>(r0 + j) * E] = run;
+      run += c[j];
+    }
+  }
+}
+
+// Places a range's slots. Each block scans the expert totals itself; the first
+// writes the offsets.
+template <int SLOTS>
+__global__ __launch_bounds__(64) void map_place_kernel(
+    const int32_t* __restrict__ ids, int nslots, int offset, int E, int key_bits,
+    const int32_t* __restrict__ range_base, const int32_t* __restrict__ counts,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ row_slot, int32_t* __restrict__ slot_row) {
+  extern __shared__ int32_t lds[];
+  const int lane = lane_id();
+  const int s0 = blockIdx.x * SLOTS, s1 = min(nslots, s0 + SLOTS);
+  const int32_t* base = range_base + static_cast<size_t>(blockIdx.x) * E;
+  int ex[SLOTS / kWave];
+  load_range(ids, s0, s1, offset, E, ex);
+  constexpr int kPer = kMaxExperts / kWave / 4;  // 64-expert groups loaded together
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += kPer * kWave) {
+    int c[kPer], b[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = e0 + i * kWave + lane;
+      c[i] = e < E ? counts[e] : 0;
+      b[i] = e < E ? base[e] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = e0 + i * kWave + lane;
+      const int incl = wave_incl_scan(c[i]);
+      const int first = run + incl - c[i];
+      if (e < E) lds[e] = first + b[i];
+      if (blockIdx.x == 0 && e < E) offsets[e] = first;
+      run += __builtin_amdgcn_readlane(incl, kWave - 1);
+    }
+  }
+  if (blockIdx.x == 0 && lane == 0) offsets[E] = run;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int g = 0; g < SLOTS / kWave; ++g) {
+    const int s = s0 + g * kWave + lane;
+    if (s0 + g * kWave < s1)  // wave-uniform
+      place_slots(s, s < s1, ex[g], key_bits, E, lds, row_slot, slot_row);
+  }
+}
+
+template <int SLOTS>
+static hipError_t launch_maps(const SortMapsArgs& a, hipStream_t st) {
   int key_bits = 1;
   while ((1 << key_bits) <= a.E) ++key_bits;  // keys 0..E inclusive
   const size_t lds = static_cast<size_t>(a.E) * sizeof(int32_t);
-  const GlobalIds ids{a.ids, a.expert_offset, a.E};
-  hipLaunchKernelGGL((sort_count_kernel<GlobalIds>), dim3(a.n_ranges), dim3(64), lds, st, ids,
-                     a.nslots, a.E, a.n_ranges, a.range_counts);
+  const int n_ranges = (a.nslots + SLOTS - 1) / SLOTS;
+  hipLaunchKernelGGL((map_count_kernel<SLOTS>), dim3(n_ranges), dim3(64), lds, st, a.ids, a.nslots,
+                     a.expert_offset, a.E, a.range_counts);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(sort_range_scan_kernel, dim3((a.E + kWave - 1) / kWave), dim3(256), 0, st,
-                     a.range_counts, a.n_ranges, a.E, a.counts);
+  hipLaunchKernelGGL(map_scan_kernel, dim3((a.E + kWave - 1) / kWave), dim3(64 * kMapWaves), 0, st, a.range_counts, n_ranges, a.E, a.counts);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(sort_offsets_kernel, dim3(1), dim3(1024), 0, st, a.E, a.counts, a.offsets);
-  err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((sort_scatter_kernel<GlobalIds>), dim3(a.n_ranges), dim3(64), lds, st, ids,
-                     a.nslots, a.E, a.n_ranges, key_bits, a.range_counts, a.offsets, a.sorted_slot,
-                     a.expanded_idx);
+  hipLaunchKernelGGL((map_place_kernel<SLOTS>), dim3(n_ranges), dim3(64), lds, st, a.ids, a.nslots,
+                     a.expert_offset, a.E, key_bits, a.range_counts, a.counts, a.offsets,
+                     a.row_slot, a.slot_row);
   return hipGetLastError();
+}
+
+hipError_t launch_sort_maps(const SortMapsArgs& a, hipStream_t st) {
+  return map_range_slots(a.nslots) == kShortRange ? launch_maps<kShortRange>(a, st)
+                                                  : launch_maps<kRangeSlots>(a, st);
 }
 
 }  // namespace moe

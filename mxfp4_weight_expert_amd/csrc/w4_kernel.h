@@ -175,7 +175,7 @@ __device__ __forceinline__ int opaque(int v) {
 // none; weights alone stream at 7.1 TB/s. Tokens loaded a KB at a time and
 // passed through LDS took 151 to 142 us.
 template <int FMT, int G, int DT, int MT, int RB, int W>
-__global__ __launch_bounds__(64 * W, W == 8 || MT == 2 ? 2 : MT == 1 ? 3 : 1) void w4_kernel(W4Args a) {
+__global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W4Args a) {
   constexpr int L = w4_layout(FMT, G, DT);
   constexpr bool kInt = FMT == MOE_W4_INT4;
   constexpr bool kFold = FMT == MOE_W4_MXFP4 && DT == MOE_DTYPE_BF16;  // scale in the convert
