@@ -50,7 +50,7 @@ extern "C" {
  *   dtype          MOE_DTYPE_* of the rows; sums are held in 32 bits and
  *                  rounded once, to the nearest even
  *
- * T * topk is at most 2^23 slots. Slot t * topk + k is column k of token t.
+ * T * topk is at most 2^23 slots, T * H at most 2^33. Slot t * topk + k is column k of token t.
  */
 typedef struct moe_ops_dispatch_shape {
   int32_t T;
@@ -65,7 +65,7 @@ typedef struct moe_ops_dispatch_shape {
  * Check a shape and return the workspace bytes that moe_ops_dispatch needs
  * (at least 256). Host only. MOE_ERR_INVALID: null pointer, T < 0, E, topk or
  * H < 1, expert_offset < 0; MOE_ERR_UNSUPPORTED: topk > 32, E > 2048,
- * T * topk > 2^23, H > 2^24, unknown dtype.
+ * T * topk > 2^23, H > 2^24, T * H > 2^33, unknown dtype.
  */
 int moe_ops_dispatch_query(const moe_ops_dispatch_shape* shape, uint64_t* workspace_bytes);
 
@@ -150,7 +150,8 @@ int moe_ops_combine_backward(const void* dout_dev, const void* rows_dev,
  * format: codes are exact in the tokens' type and a group's scale meets its
  * sum in 32 bits. With bfloat16 tokens MXFP4 scales are applied to the codes,
  * which is exact too: scale bytes up to 252 (then no weight passes the
- * type's range; bytes 253 and 254 may give infinities).
+ * type's range; bytes 253 and 254 may give infinities). INT4 zero points come
+ * off a group's sum, so an infinite x gives NaN there.
  */
 typedef struct moe_ops_w4_shape {
   int32_t M;
@@ -173,15 +174,17 @@ typedef struct moe_ops_w4_shape {
  *   w_dev       uint8 [Np, K / 2], Np = N rounded up to 16: two codes a byte,
  *               the even K in the low nibble, in the packed layout of
  *               moe_mxfp4_prepack (rows from N on may hold anything)
- *   scales_dev  uint8 [N, K / 32] E8M0 (MXFP4; 4-byte aligned) or dtype
- *               [N, K / group] (INT4), row-major
- *   zeros_dev   uint8 [N, K / group] zero points (INT4), or NULL: 8
+ *   scales_dev  uint8 [N, K / 32] E8M0 (MXFP4) or dtype [N, K / group] (INT4),
+ *               row-major, 4-byte aligned
+ *   zeros_dev   uint8 [N, K / group] zero points (INT4; 4-byte aligned), or
+ *               NULL: 8
  *   bias_dev    dtype [N], or NULL
  *   out_dev     out_dtype [M, N] rows ldo apart; nothing between them is written
  *
  * MOE_ERR_INVALID: null or misaligned pointers, sizes below their range,
- * strides shorter than a row, zeros with MXFP4, E != 1; MOE_ERR_UNSUPPORTED:
- * K % 128, K > 8192, N > 2^24, M > 2^23, unknown format, group or type.
+ * strides shorter than a row, ldx % 8, zeros with MXFP4, E != 1;
+ * MOE_ERR_UNSUPPORTED: K % 128, K > 8192, N, ldx or ldo > 2^24, M > 2^23,
+ * (M / 16 + E + 1) * (N / 16 + 1) >= 2^31, unknown format, group or type.
  */
 int moe_ops_w4_linear(const void* x_dev, const uint8_t* w_dev, const void* scales_dev,
                       const uint8_t* zeros_dev, const void* bias_dev,

@@ -10,7 +10,9 @@ namespace {
 
 constexpr int64_t kMaxSlots = int64_t{1} << 23;
 constexpr int64_t kMaxRowLen = int64_t{1} << 24;  // H, N, ldx, ldo
-constexpr int64_t kMaxElems = int64_t{1} << 38;   // T * H: bounds the grids
+// T * H: keeps the grids (a one-wave block for 1 KB of a token) within the 2^32
+// threads of a launch
+constexpr int64_t kMaxElems = int64_t{1} << 33;
 
 bool known_dtype(int d) {
   return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16 || d == MOE_DTYPE_FP32;

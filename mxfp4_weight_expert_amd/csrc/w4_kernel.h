@@ -303,7 +303,7 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
       // The blocks of an XCD take a row tile's steps from different places on:
       // in step, all of them would ask one L2 channel for the same tokens, whose
       // rows are often a multiple of the channels' span apart.
-      const int turn = ((item >> 3) + kpart * (nsteps >> 2)) % nsteps;
+      const int turn = ((item >> 3) + kpart * (nsteps >> 2)) % max(nsteps, 1);
       auto place = [&](int step) { return step + turn < nsteps ? step + turn : step + turn - nsteps; };
       auto load = [&](int d, int step) {  // step: wave-uniform
         const bool in = step < nsteps;

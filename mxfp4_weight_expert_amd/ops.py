@@ -2,13 +2,15 @@
 tokens by expert with their gradients, and few-row products with 4-bit weights.
 
 Argument checks and marshalling only; every step runs in the library's HIP
-kernels, on the current stream of the tensors' device unless `stream` (a raw
-stream handle of that device) is given. Outputs are allocated when not given.
+kernels, on the current stream of the tensors' device or on `stream` (a raw
+stream handle of that device), which has to be ordered after the inputs' writers.
+Outputs and the workspace are allocated, for that stream, when not given.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from dataclasses import dataclass
 
 from . import MOE_OK, MoeError, load_library
@@ -163,14 +165,37 @@ def _result(t, what: str, shape: tuple, dtype, device):
     return t
 
 
-def _run(name: str, device, stream, *args):
-    """Call an entry point with `device` current (the library launches there)."""
+def _with_stream(fn):
+    """Gives an operator its `stream` argument: that stream is the current one
+    during the call, so that what the call allocates belongs to it."""
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+
+        device = (args[0] if args else next(iter(kw.values()))).device
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU, got {device}")
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            return fn(*args, **kw)
+
+    sig = inspect.signature(fn)
+    call.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(),
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
+    return call
+
+
+def _run(name: str, device, *args):
+    """Call an entry point on the device's current stream, with `device` current
+    (the library launches there)."""
     import torch
 
     if device.type != "cuda":
         raise ValueError(f"tensors must be on the GPU, got {device}")
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch._C._cuda_getDevice():
         rc = _entry(name)(*args, stream)
     else:
@@ -189,8 +214,9 @@ def dispatch_query(shape: DispatchShape) -> int:
     return int(n.value)
 
 
+@_with_stream
 def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_slot=None,
-             slot_row=None, workspace=None, stream=None):
+             slot_row=None, workspace=None):
     """Token rows into expert order; returns (rows, offsets, row_slot, slot_row).
 
     x [T, H]; topk_ids int32 [T, topk] global ids, those outside
@@ -214,13 +240,14 @@ def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_s
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         _check(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    _run("dispatch", dev, stream, x.data_ptr(), topk_ids.data_ptr(), shape._c, out.data_ptr(),
+    _run("dispatch", dev, x.data_ptr(), topk_ids.data_ptr(), shape._c, out.data_ptr(),
          offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(), workspace.data_ptr(),
          workspace.numel())
     return out, offsets, row_slot, slot_row
 
 
-def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None, stream=None):
+@_with_stream
+def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None):
     """Gradient of dispatch with respect to x: drows [T * topk, H] -> [T, H]."""
     import torch
 
@@ -229,12 +256,13 @@ def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None, stream
     _check(drows, "drows", sorted_rows, dt, dev)
     _check(slot_row, "slot_row", maps, torch.int32, dev)
     out = _result(out, "out", tokens, dt, dev)
-    _run("dispatch_backward", dev, stream, drows.data_ptr(), slot_row.data_ptr(), shape._c,
+    _run("dispatch_backward", dev, drows.data_ptr(), slot_row.data_ptr(), shape._c,
          out.data_ptr())
     return out
 
 
-def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None, stream=None):
+@_with_stream
+def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None):
     """Rows back to token order: out[t] = sum_k topk_w[t, k] * rows[slot_row[t, k]].
 
     rows [T * topk, H]; slot_row as dispatch gives it; topk_w float32 [T, topk].
@@ -247,13 +275,13 @@ def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None, stream=No
     _check(slot_row, "slot_row", maps, torch.int32, dev)
     _check(topk_w, "topk_w", maps, torch.float32, dev)
     out = _result(out, "out", tokens, dt, dev)
-    _run("combine", dev, stream, rows.data_ptr(), slot_row.data_ptr(), topk_w.data_ptr(), shape._c,
+    _run("combine", dev, rows.data_ptr(), slot_row.data_ptr(), topk_w.data_ptr(), shape._c,
          out.data_ptr())
     return out
 
 
-def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=None, dw=None,
-                     stream=None):
+@_with_stream
+def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=None, dw=None):
     """Gradients of combine from dout [T, H]: (drows [T * topk, H], dtopk_w
     float32 [T, topk]). Rows that no slot names stay as they were in `dy`;
     weights without a row get 0."""
@@ -267,12 +295,12 @@ def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=N
     _check(topk_w, "topk_w", maps, torch.float32, dev)
     dy = _result(dy, "dy", sorted_rows, dt, dev)
     dw = _result(dw, "dw", maps, torch.float32, dev)
-    _run("combine_backward", dev, stream, dout.data_ptr(), rows.data_ptr(), slot_row.data_ptr(),
+    _run("combine_backward", dev, dout.data_ptr(), rows.data_ptr(), slot_row.data_ptr(),
          topk_w.data_ptr(), shape._c, dy.data_ptr(), dw.data_ptr())
     return dy, dw
 
 
-def _w4(name, x, offsets, w, scales, shape, zeros, bias, out, stream):
+def _w4(name, x, offsets, w, scales, shape, zeros, bias, out):
     import torch
 
     dev = x.device
@@ -297,11 +325,12 @@ def _w4(name, x, offsets, w, scales, shape, zeros, bias, out, stream):
     if offsets is not None:
         _check(offsets, "offsets", (shape.E + 1,), torch.int32, dev)
         args.insert(0, offsets.data_ptr())
-    _run(name, dev, stream, x.data_ptr(), *args)
+    _run(name, dev, x.data_ptr(), *args)
     return out
 
 
-def w4_linear(x, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None, stream=None):
+@_with_stream
+def w4_linear(x, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None):
     """out = x @ weight.T (+ bias) for a few rows of x and one 4-bit matrix.
 
     x [M, K] in shape.dtype (rows may be strided, multiples of 8 elements);
@@ -310,15 +339,15 @@ def w4_linear(x, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None, 
     zeros uint8 [N, K / group] (int4; None: 8); bias [N]. The matrix arrays may
     carry a leading 1. out [M, N] in shape.out_dtype (rows may be strided).
     """
-    return _w4("w4_linear", x, None, w, scales, shape, zeros, bias, out, stream)
+    return _w4("w4_linear", x, None, w, scales, shape, zeros, bias, out)
 
 
-def w4_grouped_linear(x, offsets, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None,
-                      stream=None):
+@_with_stream
+def w4_grouped_linear(x, offsets, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None):
     """Rows [offsets[e], offsets[e + 1]) of x times matrix e, as w4_linear.
 
     offsets int32 [E + 1] (as dispatch returns them); w [E, Np, K / 2]; scales
     and zeros [E, N, K / group]; bias [E, N]. Rows of out that no expert owns
     stay as they were.
     """
-    return _w4("w4_grouped_linear", x, offsets, w, scales, shape, zeros, bias, out, stream)
+    return _w4("w4_grouped_linear", x, offsets, w, scales, shape, zeros, bias, out)

@@ -77,7 +77,8 @@ def ref_weights(codes, scales, zeros, fmt, group):
         z = np.repeat(np.full(scales.shape, 8.0) if zeros is None else zeros.astype(np.float64), group, -1)
         s, v, m = scales, codes - z, codes + z
     s = np.repeat(s, group, -1)
-    return v * s, m * np.abs(s)
+    with np.errstate(invalid="ignore"):  # 0 times an infinite scale
+        return v * s, m * np.abs(s)
 
 
 def sum_tol(K: int) -> float:

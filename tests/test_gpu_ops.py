@@ -1,5 +1,9 @@
 """Dispatch, combine and the 4-bit products against 64-bit references, at the
 sizes, maps and layouts where they can go wrong."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -542,6 +546,108 @@ def test_training_step_repeats_bit_for_bit():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {i}"
         assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
+def test_stream_argument():
+    """Calls on a stream given by its handle, which allocate their outputs, while
+    the current stream is another: in order on theirs, and as on the default one."""
+    T, topk, E, H, N = 700, 8, 16, 512, 640
+    rng = np.random.default_rng(21)
+    ids = torch.from_numpy(_ids(rng, T, topk, E)).cuda()
+    shape = moe.DispatchShape(T=T, E=E, topk=topk, H=H)
+    m, _ = _matrix(rng, E, N, H, "mxfp4", 32, "bf16", False)
+    ws = moe.W4Shape(M=T * topk, N=N, K=H, E=E)
+    back = moe.DispatchShape(T=T, E=E, topk=topk, H=N)
+    x, w = torch.randn(T, H, device="cuda").to(torch.bfloat16), torch.rand(T, topk, device="cuda")
+
+    def chain(**kw):
+        rows, off, _, slot_row = moe.dispatch(x, ids, shape, **kw)
+        return moe.combine(moe.w4_grouped_linear(rows, off, m["w"], m["scales"], ws, **kw), slot_row, w, back, **kw)
+
+    want = chain()
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(3)]
+    got = [chain(stream=s.cuda_stream) for s in side for _ in range(3)]  # three chains at once
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_first_call_inside_a_capture():
+    # a process whose first call of every operator is captured
+    code = """
+import torch, mxfp4_weight_expert_amd as moe
+x = torch.randn(6, 256, device="cuda").to(torch.bfloat16)
+ids = torch.tensor([[0, 1]] * 6, dtype=torch.int32, device="cuda")
+w = torch.ones(6, 2, device="cuda")
+s = moe.DispatchShape(T=6, E=2, topk=2, H=256)
+ws = moe.W4Shape(M=12, N=32, K=256, E=2, out_dtype="fp32")
+c = torch.randint(0, 256, (2, 32, 128), dtype=torch.uint8, device="cuda")
+sc = torch.full((2, 32, 8), 127, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+def run():
+    rows, off, _, back = moe.dispatch(x, ids, s)
+    y = moe.w4_grouped_linear(rows, off, c, sc, ws)
+    out = moe.combine(rows, back, w, s)
+    d, dw = moe.combine_backward(out, rows, back, w, s)
+    return y, out, d, dw, moe.dispatch_backward(d, back, s)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+for _ in range(3):
+    g.replay()
+    want = run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_rows_past_32_bit_offsets():
+    # 655,360 rows of 8 KB: 5.4 GB of rows, with a twin of the last token's slots
+    T, topk, E, H = 20480, 32, 40, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(topk, 1).indices.to(torch.int32)
+    shape = moe.DispatchShape(T=T, E=E, topk=topk, H=H)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    rows, off, row_slot, slot_row = moe.dispatch(x, ids, shape)
+    order = torch.sort(ids.view(-1).long() * (T * topk) + torch.arange(T * topk, device="cuda")).values % (T * topk)
+    assert torch.equal(row_slot.long(), order) and int(off[-1]) == T * topk
+    at = torch.cat([torch.arange(0, T * topk, 997, device="cuda"), torch.arange(T * topk - 64, T * topk, device="cuda")])
+    assert torch.equal(rows[at], x[order[at] // topk])
+    w = torch.ones(T, topk, device="cuda")
+    out = moe.combine(rows, slot_row, w, shape)
+    t = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    # topk equal terms: exact sums of up to 32 copies but for the last rounding
+    assert torch.equal(out[t], (x[t].float() * topk).to(torch.bfloat16))
+    drows, dw = moe.combine_backward(x, rows, slot_row, w, shape)
+    assert torch.equal(drows[at], rows[at])
+    ref = (f64(x[t]) ** 2).sum(1)[:, None].repeat(topk, 1)
+    _close(dw[t], ref, (H / 64 + 16) * 2.0 ** -24 * ref, "dtopk_w")
+
+
+def test_weights_past_32_bit_offsets():
+    # 130 matrices of 8192 x 8192: 4.4 GB of codes; rows for the first and last
+    E, N, K = 130, 8192, 8192
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    sc = torch.randint(118, 128, (E, N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(6, K, generator=g, device="cuda").to(torch.bfloat16)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:], off[-2], off[-1] = 2, 3, 6
+    got = moe.w4_grouped_linear(x, off, w, sc, moe.W4Shape(M=6, N=N, K=K, E=E, out_dtype="fp32"))
+    one = moe.W4Shape(M=6, N=N, K=K, out_dtype="fp32")
+    for e, lo, hi in ((0, 0, 2), (E - 2, 2, 3), (E - 1, 3, 6)):
+        alone = moe.w4_linear(x, w[e].clone(), sc[e].clone(), one)[lo:hi]
+        codes = w[e].view(N // 16, K // 128, 16, 64).transpose(1, 2).reshape(N, K // 2)[-32:]
+        codes = torch.stack([codes & 15, codes >> 4], -1).view(32, K).cpu().numpy()
+        W, mag = ref_weights(codes, sc[e, -32:].cpu().numpy(), None, "mxfp4", 32)
+        ref, size = f64(x[lo:hi]) @ W.T, np.abs(f64(x[lo:hi])) @ mag.T
+        tol = round_tol(ref, "fp32", sum_tol(K) * size)
+        _close(got[lo:hi, -32:], ref, tol, f"matrix {e}")
+        _close(alone[:, -32:], ref, tol, f"matrix {e} alone")
 
 
 def test_binding_refusals_on_the_gpu():

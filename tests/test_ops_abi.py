@@ -54,7 +54,7 @@ def _ds(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), 1), (dict(E=0), 1), (dict(topk=0), 1), (dict(H=0), 1), (dict(expert_offset=-1), 1),
     (dict(topk=33), 2), (dict(E=2049), 2), (dict(H=(1 << 24) + 1), 2), (dict(T=(1 << 19) + 1), 2),
-    (dict(T=1 << 15, topk=1, H=1 << 24), 2),
+    (dict(T=1 << 15, topk=1, H=1 << 24), 2), (dict(T=1 << 20, topk=1, H=(1 << 13) + 1), 2),
 ])
 def test_dispatch_query_refuses(kw, code):
     with pytest.raises(moe.MoeError) as ei:
@@ -192,8 +192,11 @@ def test_w4_refuses_before_launch():
 def test_binding_refuses_host_tensors_and_wrong_layouts():
     s = _ds(T=2, E=4, topk=2, H=8)
     x, ids = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32)
-    with pytest.raises(ValueError, match="GPU"):
-        moe.dispatch(x, ids, s)
+    for kw in ({}, {"stream": 0}):
+        with pytest.raises(ValueError, match="GPU"):
+            moe.dispatch(x, ids, s, **kw)
+        with pytest.raises(ValueError, match="GPU"):
+            moe.dispatch(x=x, topk_ids=ids, shape=s, **kw)
     with pytest.raises(ValueError, match="topk_ids"):
         moe.dispatch(x, ids.long(), s)
     with pytest.raises(ValueError, match="contiguous"):
