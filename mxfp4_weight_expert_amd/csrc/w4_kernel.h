@@ -36,6 +36,11 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
+// Non-temporal 16-byte buffer load (cache-policy operand 2), for weights read once.
+__device__ __forceinline__ uint4 bld16nt(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));
+}
+
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
   const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
   a = r[0];
