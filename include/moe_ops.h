@@ -86,7 +86,7 @@ int moe_ops_dispatch_query(const moe_ops_dispatch_shape* shape, uint64_t* worksp
  *
  * Deterministic. T = 0 writes zeros to offsets and reads nothing. Alignment:
  * rows their element size, maps 4 bytes, workspace 256 bytes.
- * MOE_ERR_WORKSPACE: workspace NULL with a size > 0 needed, too small or misaligned. Calls that
+ * MOE_ERR_WORKSPACE: workspace NULL, too small or misaligned. Calls that
  * may overlap in time need workspaces of their own (two captured graphs that
  * can run at once among them).
  */
@@ -168,7 +168,8 @@ typedef struct moe_ops_w4_shape {
 
 /*
  * A few tokens times one matrix (E = 1). Made for decode: the weights are
- * read once for up to 64 rows of x; more rows are taken 64 at a time.
+ * read once for up to 64 rows of x (INT4 with groups of 32: 16, beyond 32 rows);
+ * more rows are taken that many at a time.
  *
  *   x_dev       [M, K] rows ldx apart, 16-byte aligned, ldx % 8 == 0
  *   w_dev       uint8 [Np, K / 2], Np = N rounded up to 16: two codes a byte,
@@ -196,8 +197,8 @@ int moe_ops_w4_linear(const void* x_dev, const uint8_t* w_dev, const void* scale
  * >= 0, as moe_ops_dispatch writes them; values past M count as M. Rows of out
  * that no expert owns are left as they were, those of x are not read.
  * w [E, Np, K / 2], scales and zeros [E, N, K / group], bias [E, N]: the
- * matrices of w4_linear one after another. Meant for few rows an expert; an
- * expert's weights are read once for up to 16, 32 or 64 of its rows, by M / E.
+ * matrices of w4_linear one after another. Meant for few rows an expert: an
+ * expert's weights are read once for 16 of its rows (64 where M / E is large).
  */
 int moe_ops_w4_grouped_linear(const void* x_dev, const int32_t* offsets_dev, const uint8_t* w_dev,
                               const void* scales_dev, const uint8_t* zeros_dev,

@@ -292,9 +292,10 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[b][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // The wave's K steps. XL: 1 KB loads of tokens a step, four rows each.
+    // The wave's K steps. XL: 1 KB loads of tokens a step, four rows each; TT:
+    // 16-row tiles that hold rows (an expert may have fewer than MT).
     auto walk = [&](auto xlc) {
-      constexpr int XL = decltype(xlc)::value;
+      constexpr int XL = decltype(xlc)::value, TT = XL <= 4 ? 1 : XL / 4;
       const int ln = opaque(lane), r = ln & 15, q = ln >> 4;
       const uint32_t woff = k0 * kPkBlock + r * 64 + q * 16;
       uint4 xg[D][XL], w[D][RB];
@@ -331,10 +332,10 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
 #pragma unroll
         for (int i = 0; i < XL; ++i) *reinterpret_cast<uint4*>(s_tok + xlds[i]) = xg[d][i];
         __builtin_amdgcn_wave_barrier();
-        uint4 xf[MT][4];
-        float xs[MT];  // lane (m, q): of the sum of row m's tokens, INT4
+        uint4 xf[TT][4];
+        float xs[TT];  // lane (m, q): of the sum of row m's tokens, INT4
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < TT; ++t) {
           const uint32_t m = XL < 4 ? r & (4 * XL - 1) : t * 16 + r;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
             for (int j = 0; j < 4; ++j) {
               const uint4 f = __builtin_bit_cast(uint4, decode_fp4x8(dw[j], s));
 #pragma unroll
-              for (int t = 0; t < MT; ++t) acc[b][t] = mfma_rows<DT>(xf[t][j], f, acc[b][t]);
+              for (int t = 0; t < TT; ++t) acc[b][t] = mfma_rows<DT>(xf[t][j], f, acc[b][t]);
             }
           } else {
             constexpr int kPer = 4 / kGroups;  // MFMAs a group's sum takes
@@ -390,14 +391,14 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
               swap32(dw[0], dw[2]);
               swap32(dw[1], dw[3]);
             }
-            f32x4_t part[MT];
+            f32x4_t part[TT];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint4 f;
               if constexpr (kInt) f = decode_int4x8<DT>(dw[j]);
               else f = decode_fp4x8_f16(dw[j]);
 #pragma unroll
-              for (int t = 0; t < MT; ++t) {
+              for (int t = 0; t < TT; ++t) {
                 if (j % kPer == 0) part[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
                 part[t] = mfma_rows<DT>(xf[t][j], f, part[t]);
                 if (j % kPer == kPer - 1) {
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
 #pragma unroll
               for (int g = 1; g < kGroups; ++g) sq = gq == g ? s[g] : sq;
 #pragma unroll
-              for (int t = 0; t < MT; ++t)
+              for (int t = 0; t < TT; ++t)
                 acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xs[t], -sq * z, acc[b][t], 0, 0, 0);
             }
           }
@@ -430,12 +431,14 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
         }
       }
     };
-    if constexpr (MT > 1) {
-      walk(std::integral_constant<int, 4 * MT>{});
+    if constexpr (MT == 2) {
+      walk(std::integral_constant<int, 8>{});
     } else {
       if (rows <= 4) walk(std::integral_constant<int, 1>{});
       else if (rows <= 8) walk(std::integral_constant<int, 2>{});
-      else walk(std::integral_constant<int, 4>{});
+      else if (MT == 1 || rows <= 16) walk(std::integral_constant<int, 4>{});
+      else if (rows <= 32) walk(std::integral_constant<int, 4 * std::min(MT, 2)>{});
+      else walk(std::integral_constant<int, 4 * MT>{});
     }
 
     // Join the waves that share weight rows, and store: value (m, n) of a tile
@@ -526,28 +529,40 @@ void w4_go(const W4Args& a, hipStream_t st) {
 //   and 15.3 with RB = 1, 13.4 and 15.6 with RB = 4 and four waves. 4096 x 4096:
 //   5.6 and 7.2, 4.8 and 6.1, 8.4 and 9.7. 24576 x 2048, one token: 7.2 with RB = 2
 //   and four waves, 8.8 with RB = 4.
-// Row tiles (MT) go by the rows an expert has on average.
+// Row tiles of x a task takes (MT): 16 rows, whose tiles read their weights again
+// from the caches, or 32 (up to 32 rows of one matrix) or 64, which share a decode.
+// N 32768, K 4096, MXFP4, 32 and 64 rows: 28 and 42 us so, 31 and 58 in tiles of
+// 16; INT4 of 64 33 and 54, 35 and 66. INT4 of 32 runs out of registers with 64
+// rows (82 us against 75). The rows of an expert are not known here, only M / E,
+// which counts those that live elsewhere too, so experts take tiles of 16 until
+// M / E says many: K 2048 x N 4096, a quarter of 256 experts, M / E = 64 with 16
+// rows each, 84 us in tiles of 16, 133 in tiles of 64; M / E = 1024 with 256 rows
+// each (K 3584, N 768, 16 experts) 113 and 76.
 constexpr int kW4Kw1Scales = 36 << 10;  // with 16 KB of tokens, three blocks in a CU's LDS
 template <int FMT, int G, int DT>
 void w4_rows(const W4Args& a0, hipStream_t st) {
   W4Args a = a0;
+  constexpr bool kWide = !(FMT == MOE_W4_INT4 && G == 32);
   const bool grouped = a.offsets != nullptr;
-  const int per = grouped ? (a.M + a.E - 1) / a.E : a.M;
+  int mt = grouped ? (a.M / a.E > 128 ? 4 : 1) : a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+  if (mt == 4 && !kWide) mt = 1;
   const int64_t U = static_cast<int64_t>((a.N + 15) / 16) * (grouped ? std::min(a.E, a.M) : 1);
   const int nk = a.K >> 7;
   a.kw = 4;
   // scale rows (and zero points) of a kw = 1 block's RB * 64 weight rows in LDS
-  const int scales = (per > 16 ? 128 : 256) * nk * (128 / G) *
+  const int scales = (mt > 1 ? 128 : 256) * nk * (128 / G) *
                      (a.format == MOE_W4_MXFP4 ? 1 : a.zeros != nullptr ? 3 : 2);
   if (U >= 2048 && scales <= kW4Kw1Scales) {
     constexpr int64_t kBlocks = 256 * 3;  // resident, as a rule
     const auto cost = [&](int64_t tasks, int steps) { return (tasks + kBlocks - 1) / kBlocks * (steps + 4); };
     if (cost(U / 16, nk) <= cost(U / 4, (nk + 3) / 4)) a.kw = 1;
   }
-  if (per > 32) {
-    if (U >= 512) w4_go<FMT, G, DT, 4, 2, 4>(a, st);
-    else w4_go<FMT, G, DT, 4, 1, 4>(a, st);
-  } else if (per > 16) {
+  if (mt == 4) {
+    if constexpr (kWide) {
+      if (U >= 512) w4_go<FMT, G, DT, 4, 2, 4>(a, st);
+      else w4_go<FMT, G, DT, 4, 1, 4>(a, st);
+    }
+  } else if (mt == 2) {
     if (U >= 512) w4_go<FMT, G, DT, 2, 2, 4>(a, st);
     else w4_go<FMT, G, DT, 2, 1, 4>(a, st);
   } else if (U >= 2048) {

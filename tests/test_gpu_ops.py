@@ -278,6 +278,8 @@ LINEAR = [
     (6, 200000, 128, "int4", 64, "fp16", "fp16", True, False),
     (20, 40001, 256, "int4", 128, "bf16", "bf16", False, False),
     (50, 40001, 256, "mxfp4", 32, "fp16", "fp32", False, False),
+    (70, 9000, 2048, "int4", 128, "fp16", "fp16", True, False),
+    (49, 900, 1024, "int4", 32, "bf16", "fp32", True, True),
     # K over eight waves
     (9, 5000, 2176, "int4", 64, "bf16", "fp32", False, True),
     (12, 40, 7168, "int4", 32, "fp16", "fp32", True, False),
@@ -380,6 +382,10 @@ GROUPED = [
     ([2] * 100, 700, 20, 384, "mxfp4", 32, "fp16", "fp32", False, False),
     ([33, 34, 31, 0, 90], 0, 100, 1536, "mxfp4", 32, "bf16", "bf16", False, False),
     ([5, 1, 0, 3], 100, 768, 3584, "mxfp4", 32, "bf16", "fp32", False, False),
+    # many rows an expert: tiles of 64, their ragged ends
+    ([400, 0, 17, 70, 33, 1, 5, 330], 200, 50, 1152, "mxfp4", 32, "fp16", "fp32", False, True),
+    ([300, 40], 30, 600, 256, "int4", 64, "bf16", "bf16", True, False),
+    ([300, 40], 30, 600, 256, "int4", 32, "bf16", "bf16", True, False),
     # one wave a weight group's K, and zero points and scales that would not fit LDS then
     ([1, 0, 3, 5, 9, 2] * 20, 3, 500, 384, "int4", 32, "bf16", "fp32", True, True),
     ([2, 1] * 8, 0, 4096, 8192, "int4", 32, "fp16", "fp32", True, False),
