@@ -36,9 +36,14 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
-// Non-temporal 16-byte buffer load (cache-policy operand 2), for weights read once.
-__device__ __forceinline__ uint4 bld16nt(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));
+// 16-byte buffer load of weights, non-temporal (cache-policy operand 2) where
+// they are read once: 64-token decode of 896 experts 143 us against 164 with
+// plain loads. Where several row tiles read them (64 experts of 32 rows) plain
+// loads take 127 us, these 135; a branch around the two kinds of load costs the
+// first case 6 % (its waits then cover both), so the walk is an instance of each.
+template <bool ONCE>
+__device__ __forceinline__ uint4 bld16_once(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, ONCE ? 2 : 0));
 }
 
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
@@ -241,6 +246,7 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
 
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     int e = 0, tn, row0, rows;
+    bool once = tiles == 1;  // the weights are read by this task alone: past the caches
     if (a.offsets == nullptr) {
       // row tiles of the same weights are neighbours: the second's come from L2
       tn = item / tiles;
@@ -255,7 +261,8 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
         else hi = mid - 1;
       }
       e = __builtin_amdgcn_readfirstlane(lo);
-      const int first = s_first[e], te = s_first[e + 1] - first;
+      const int first = s_first[e], te = __builtin_amdgcn_readfirstlane(s_first[e + 1] - first);
+      once = te == 1;
       const int local = item - first * ntn;
       tn = local / te;
       const int m = local - tn * te;
@@ -294,8 +301,9 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
 
     // The wave's K steps. XL: 1 KB loads of tokens a step, four rows each; TT:
     // 16-row tiles that hold rows (an expert may have fewer than MT).
-    auto walk = [&](auto xlc) {
+    auto walk = [&](auto xlc, auto oncec) {
       constexpr int XL = decltype(xlc)::value, TT = XL <= 4 ? 1 : XL / 4;
+      constexpr bool ONCE = decltype(oncec)::value;
       const int ln = opaque(lane), r = ln & 15, q = ln >> 4;
       const uint32_t woff = k0 * kPkBlock + r * 64 + q * 16;
       uint4 xg[D][XL], w[D][RB];
@@ -318,7 +326,7 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
         for (int i = 0; i < XL; ++i) xg[d][i] = bld16(xb, in ? xoff[i] + at * 256 : kNoRow);
 #pragma unroll
         for (int b = 0; b < RB; ++b)
-          w[d][b] = bld16nt(wb, in ? woff + b * gbytes + at * kPkBlock : kNoRow);
+          w[d][b] = bld16_once<ONCE>(wb, in ? woff + b * gbytes + at * kPkBlock : kNoRow);
       };
 #pragma unroll
       for (int d = 0; d < D; ++d) load(d, d);
@@ -431,15 +439,16 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
         }
       }
     };
-    if constexpr (MT == 2) {
-      walk(std::integral_constant<int, 8>{});
-    } else {
-      if (rows <= 4) walk(std::integral_constant<int, 1>{});
-      else if (rows <= 8) walk(std::integral_constant<int, 2>{});
-      else if (MT == 1 || rows <= 16) walk(std::integral_constant<int, 4>{});
-      else if (rows <= 32) walk(std::integral_constant<int, 4 * std::min(MT, 2)>{});
-      else walk(std::integral_constant<int, 4 * MT>{});
-    }
+    const auto by_rows = [&](auto oncec) {
+      if (rows <= 4) walk(std::integral_constant<int, 1>{}, oncec);
+      else if (rows <= 8) walk(std::integral_constant<int, 2>{}, oncec);
+      else if (MT == 1 || rows <= 16) walk(std::integral_constant<int, 4>{}, oncec);
+      else if (rows <= 32) walk(std::integral_constant<int, 4 * std::min(MT, 2)>{}, oncec);
+      else walk(std::integral_constant<int, 4 * MT>{}, oncec);
+    };
+    if constexpr (MT == 2) walk(std::integral_constant<int, 8>{}, std::true_type{});  // 17 to 32 rows in all
+    else if (once) by_rows(std::true_type{});
+    else by_rows(std::false_type{});
 
     // Join the waves that share weight rows, and store: value (m, n) of a tile
     // is register m % 4 of lane (n, m / 4).
