@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import inspect
 from dataclasses import dataclass
 
 from . import MOE_OK, MoeError, load_library
@@ -33,7 +32,11 @@ class _W4Shape(ctypes.Structure):
                                                                ("ldo", ctypes.c_int64)]
 
 
+torch = None  # imported by the first call: the binding itself needs none
+
+
 def _torch_dtype(name: str):
+    global torch
     import torch
 
     return getattr(torch, _TORCH_NAME[name])
@@ -101,8 +104,6 @@ class W4Shape:
     @functools.cached_property
     def _torch(self):
         """Types of x, the scales and out."""
-        import torch
-
         dt = _torch_dtype(self.dtype)
         return dt, torch.uint8 if self.format == "mxfp4" else dt, _torch_dtype(self.out_dtype or self.dtype)
 
@@ -132,74 +133,53 @@ def _entry(name: str):
     return fn
 
 
-def _check(t, what: str, shape: tuple, dtype, device):
+def _refuse(t, what: str, shape: tuple, dtype, index: int, layout: str):
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the first tensor on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t.get_device() != index:
+        first = f"GPU {index}" if index >= 0 else "the CPU"
+        raise ValueError(f"{what} is on {t.device}, the first tensor on {first}")
+    raise ValueError(f"{what} must {layout}")
 
 
-def _row_stride(t, what: str, shape: tuple, dtype, device) -> int:
+def _check(t, what: str, shape: tuple, dtype, index: int) -> int:
+    """A contiguous tensor's address. index: the GPU of the call's first tensor."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, what, shape, dtype, index, "be contiguous")
+
+
+def _row_stride(t, what: str, shape: tuple, dtype, index: int) -> int:
     """Elements between the rows of a matrix whose rows are contiguous; 0 where
     the rows follow each other."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{what} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the first tensor on {device}")
-    if t.is_contiguous():
-        return 0
-    if (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
-        raise ValueError(f"{what} must have contiguous rows that do not overlap")
-    return t.stride(0) if shape[0] > 1 else 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        if t.is_contiguous():
+            return 0
+        if (shape[1] <= 1 or t.stride(1) == 1) and (shape[0] <= 1 or t.stride(0) >= shape[1]):
+            return t.stride(0) if shape[0] > 1 else 0
+    _refuse(t, what, shape, dtype, index, "have contiguous rows that do not overlap")
 
 
-def _result(t, what: str, shape: tuple, dtype, device):
-    """The caller's output, checked, or a new one."""
-    if t is None:
-        import torch
-
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, what, shape, dtype, device)
-    return t
-
-
-def _with_stream(fn):
-    """Gives an operator its `stream` argument: that stream is the current one
-    during the call, so that what the call allocates belongs to it."""
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        import torch
-
-        device = (args[0] if args else next(iter(kw.values()))).device
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on the GPU, got {device}")
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-            return fn(*args, **kw)
-
-    sig = inspect.signature(fn)
-    call.__signature__ = sig.replace(parameters=[
-        *sig.parameters.values(),
-        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
-    return call
-
-
-def _run(name: str, device, *args):
-    """Call an entry point on the device's current stream, with `device` current
-    (the library launches there)."""
+def _on_stream(stream: int, t):
+    """`stream` as the current one, so that what a call allocates belongs to it."""
     import torch
 
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on the GPU, got {device}")
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch._C._cuda_getDevice():
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on the GPU, got {t.device}")
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device))
+
+
+def _run(name: str, index: int, *args):
+    """Call an entry point on the GPU's current stream, with that GPU current (the
+    library launches there)."""
+    if index < 0:
+        raise ValueError("tensors must be on the GPU")
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         rc = _entry(name)(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = _entry(name)(*args, stream)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_ops_" + name)
@@ -214,9 +194,8 @@ def dispatch_query(shape: DispatchShape) -> int:
     return int(n.value)
 
 
-@_with_stream
 def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_slot=None,
-             slot_row=None, workspace=None):
+             slot_row=None, workspace=None, stream=None):
     """Token rows into expert order; returns (rows, offsets, row_slot, slot_row).
 
     x [T, H]; topk_ids int32 [T, topk] global ids, those outside
@@ -225,112 +204,117 @@ def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_s
     it was; offsets int32 [E + 1]; slot_row int32 [T, topk], -1 without a row.
     workspace: uint8, at least dispatch_query(shape) bytes.
     """
-    import torch
-
-    dev, dt, i32 = x.device, shape._torch, torch.int32
-    nbytes = shape._workspace
+    dt, nbytes = shape._torch, shape._workspace
+    if stream is not None:
+        with _on_stream(stream, x):
+            return dispatch(x, topk_ids, shape, out=out, offsets=offsets, row_slot=row_slot,
+                            slot_row=slot_row, workspace=workspace)
     tokens, sorted_rows, maps = shape._arrays
-    _check(x, "x", tokens, dt, dev)
-    _check(topk_ids, "topk_ids", maps, i32, dev)
-    out = _result(out, "out", sorted_rows, dt, dev)
-    offsets = _result(offsets, "offsets", (shape.E + 1,), i32, dev)
-    row_slot = _result(row_slot, "row_slot", sorted_rows[:1], i32, dev)
-    slot_row = _result(slot_row, "slot_row", maps, i32, dev)
+    gpu, i32 = x.get_device(), torch.int32
+    px, pi = _check(x, "x", tokens, dt, gpu), _check(topk_ids, "topk_ids", maps, i32, gpu)
+    dev = x.device
+    if out is None:
+        out = torch.empty(sorted_rows, dtype=dt, device=dev)
+    if offsets is None:
+        offsets = torch.empty(shape.E + 1, dtype=i32, device=dev)
+    if row_slot is None:
+        row_slot = torch.empty(sorted_rows[0], dtype=i32, device=dev)
+    if slot_row is None:
+        slot_row = torch.empty(maps, dtype=i32, device=dev)
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    else:
-        _check(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    _run("dispatch", dev, x.data_ptr(), topk_ids.data_ptr(), shape._c, out.data_ptr(),
-         offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(), workspace.data_ptr(),
-         workspace.numel())
+    _run("dispatch", gpu, px, pi, shape._c, _check(out, "out", sorted_rows, dt, gpu),
+         _check(offsets, "offsets", (shape.E + 1,), i32, gpu),
+         _check(row_slot, "row_slot", sorted_rows[:1], i32, gpu),
+         _check(slot_row, "slot_row", maps, i32, gpu),
+         _check(workspace, "workspace", workspace.shape, torch.uint8, gpu), workspace.numel())
     return out, offsets, row_slot, slot_row
 
 
-@_with_stream
-def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None):
+def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None, stream=None):
     """Gradient of dispatch with respect to x: drows [T * topk, H] -> [T, H]."""
-    import torch
-
-    dev, dt = drows.device, shape._torch
+    dt = shape._torch
+    if stream is not None:
+        with _on_stream(stream, drows):
+            return dispatch_backward(drows, slot_row, shape, out=out)
     tokens, sorted_rows, maps = shape._arrays
-    _check(drows, "drows", sorted_rows, dt, dev)
-    _check(slot_row, "slot_row", maps, torch.int32, dev)
-    out = _result(out, "out", tokens, dt, dev)
-    _run("dispatch_backward", dev, drows.data_ptr(), slot_row.data_ptr(), shape._c,
-         out.data_ptr())
+    gpu = drows.get_device()
+    pd, ps = _check(drows, "drows", sorted_rows, dt, gpu), _check(slot_row, "slot_row", maps, torch.int32, gpu)
+    if out is None:
+        out = torch.empty(tokens, dtype=dt, device=drows.device)
+    _run("dispatch_backward", gpu, pd, ps, shape._c, _check(out, "out", tokens, dt, gpu))
     return out
 
 
-@_with_stream
-def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None):
+def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None, stream=None):
     """Rows back to token order: out[t] = sum_k topk_w[t, k] * rows[slot_row[t, k]].
 
     rows [T * topk, H]; slot_row as dispatch gives it; topk_w float32 [T, topk].
     """
-    import torch
-
-    dev, dt = rows.device, shape._torch
+    dt = shape._torch
+    if stream is not None:
+        with _on_stream(stream, rows):
+            return combine(rows, slot_row, topk_w, shape, out=out)
     tokens, sorted_rows, maps = shape._arrays
-    _check(rows, "rows", sorted_rows, dt, dev)
-    _check(slot_row, "slot_row", maps, torch.int32, dev)
-    _check(topk_w, "topk_w", maps, torch.float32, dev)
-    out = _result(out, "out", tokens, dt, dev)
-    _run("combine", dev, rows.data_ptr(), slot_row.data_ptr(), topk_w.data_ptr(), shape._c,
-         out.data_ptr())
+    gpu = rows.get_device()
+    pr, ps = _check(rows, "rows", sorted_rows, dt, gpu), _check(slot_row, "slot_row", maps, torch.int32, gpu)
+    pw = _check(topk_w, "topk_w", maps, torch.float32, gpu)
+    if out is None:
+        out = torch.empty(tokens, dtype=dt, device=rows.device)
+    _run("combine", gpu, pr, ps, pw, shape._c, _check(out, "out", tokens, dt, gpu))
     return out
 
 
-@_with_stream
-def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=None, dw=None):
+def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=None, dw=None,
+                     stream=None):
     """Gradients of combine from dout [T, H]: (drows [T * topk, H], dtopk_w
     float32 [T, topk]). Rows that no slot names stay as they were in `dy`;
     weights without a row get 0."""
-    import torch
-
-    dev, dt = dout.device, shape._torch
+    dt = shape._torch
+    if stream is not None:
+        with _on_stream(stream, dout):
+            return combine_backward(dout, rows, slot_row, topk_w, shape, dy=dy, dw=dw)
     tokens, sorted_rows, maps = shape._arrays
-    _check(dout, "dout", tokens, dt, dev)
-    _check(rows, "rows", sorted_rows, dt, dev)
-    _check(slot_row, "slot_row", maps, torch.int32, dev)
-    _check(topk_w, "topk_w", maps, torch.float32, dev)
-    dy = _result(dy, "dy", sorted_rows, dt, dev)
-    dw = _result(dw, "dw", maps, torch.float32, dev)
-    _run("combine_backward", dev, dout.data_ptr(), rows.data_ptr(), slot_row.data_ptr(),
-         topk_w.data_ptr(), shape._c, dy.data_ptr(), dw.data_ptr())
+    gpu, f32 = dout.get_device(), torch.float32
+    pd, pr = _check(dout, "dout", tokens, dt, gpu), _check(rows, "rows", sorted_rows, dt, gpu)
+    ps, pw = _check(slot_row, "slot_row", maps, torch.int32, gpu), _check(topk_w, "topk_w", maps, f32, gpu)
+    if dy is None:
+        dy = torch.empty(sorted_rows, dtype=dt, device=dout.device)
+    if dw is None:
+        dw = torch.empty(maps, dtype=f32, device=dout.device)
+    _run("combine_backward", gpu, pd, pr, ps, pw, shape._c, _check(dy, "dy", sorted_rows, dt, gpu),
+         _check(dw, "dw", maps, f32, gpu))
     return dy, dw
 
 
-def _w4(name, x, offsets, w, scales, shape, zeros, bias, out):
-    import torch
+def _matrix(t, what: str, bare: tuple, shape: tuple, dtype, gpu: int, grouped: bool):
+    """Address of a matrix array; a single matrix may come without its leading 1."""
+    if t is None:
+        return None
+    return _check(t, what, shape if grouped or t.dim() == len(shape) else bare, dtype, gpu)
 
-    dev = x.device
+
+def _w4(name, x, offsets, w, scales, shape, zeros, bias, out):
     dt, sdt, odt = shape._torch
     one, every = shape._arrays
-
-    def matrix(t, what, i, dtype):
-        if t is None:
-            return None
-        bare = offsets is None and t.dim() == len(one[i])  # one matrix, without its leading 1
-        _check(t, what, one[i] if bare else every[i], dtype, dev)
-        return t.data_ptr()
-
-    ldx, ldo = _row_stride(x, "x", (shape.M, shape.K), dt, dev), 0
+    gpu, grouped = x.get_device(), offsets is not None
+    ldx, ldo = _row_stride(x, "x", (shape.M, shape.K), dt, gpu), 0
     if out is None:
-        out = torch.empty((shape.M, shape.N), dtype=odt, device=dev)
+        out = torch.empty((shape.M, shape.N), dtype=odt, device=x.device)
     else:
-        ldo = _row_stride(out, "out", (shape.M, shape.N), odt, dev)
+        ldo = _row_stride(out, "out", (shape.M, shape.N), odt, gpu)
     cshape = ctypes.byref(shape.to_c(ldx, ldo)) if ldx or ldo else shape._c
-    args = [matrix(w, "w", 0, torch.uint8), matrix(scales, "scales", 1, sdt),
-            matrix(zeros, "zeros", 1, torch.uint8), matrix(bias, "bias", 2, dt), cshape, out.data_ptr()]
-    if offsets is not None:
-        _check(offsets, "offsets", (shape.E + 1,), torch.int32, dev)
-        args.insert(0, offsets.data_ptr())
-    _run(name, dev, x.data_ptr(), *args)
+    args = (_matrix(w, "w", one[0], every[0], torch.uint8, gpu, grouped),
+            _matrix(scales, "scales", one[1], every[1], sdt, gpu, grouped),
+            _matrix(zeros, "zeros", one[1], every[1], torch.uint8, gpu, grouped),
+            _matrix(bias, "bias", one[2], every[2], dt, gpu, grouped), cshape, out.data_ptr())
+    if grouped:
+        args = (_check(offsets, "offsets", (shape.E + 1,), torch.int32, gpu), *args)
+    _run(name, gpu, x.data_ptr(), *args)
     return out
 
 
-@_with_stream
-def w4_linear(x, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None):
+def w4_linear(x, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None, stream=None):
     """out = x @ weight.T (+ bias) for a few rows of x and one 4-bit matrix.
 
     x [M, K] in shape.dtype (rows may be strided, multiples of 8 elements);
@@ -339,15 +323,23 @@ def w4_linear(x, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None):
     zeros uint8 [N, K / group] (int4; None: 8); bias [N]. The matrix arrays may
     carry a leading 1. out [M, N] in shape.out_dtype (rows may be strided).
     """
+    if stream is not None:
+        with _on_stream(stream, x):
+            return _w4("w4_linear", x, None, w, scales, shape, zeros, bias, out)
     return _w4("w4_linear", x, None, w, scales, shape, zeros, bias, out)
 
 
-@_with_stream
-def w4_grouped_linear(x, offsets, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None):
+def w4_grouped_linear(x, offsets, w, scales, shape: W4Shape, *, zeros=None, bias=None, out=None,
+                      stream=None):
     """Rows [offsets[e], offsets[e + 1]) of x times matrix e, as w4_linear.
 
     offsets int32 [E + 1] (as dispatch returns them); w [E, Np, K / 2]; scales
     and zeros [E, N, K / group]; bias [E, N]. Rows of out that no expert owns
     stay as they were.
     """
+    if offsets is None:
+        raise ValueError("offsets are needed")
+    if stream is not None:
+        with _on_stream(stream, x):
+            return _w4("w4_grouped_linear", x, offsets, w, scales, shape, zeros, bias, out)
     return _w4("w4_grouped_linear", x, offsets, w, scales, shape, zeros, bias, out)

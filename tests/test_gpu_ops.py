@@ -660,7 +660,7 @@ def test_binding_refusals_on_the_gpu():
     shape = moe.DispatchShape(T=4, E=4, topk=2, H=16)
     x = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
     ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
-    with pytest.raises(ValueError, match="ids is on"):
+    with pytest.raises(ValueError, match="topk_ids is on cpu"):
         moe.dispatch(x, ids.cpu(), shape)
     with pytest.raises(moe.MoeError) as ei:
         moe.dispatch(x, ids, shape, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
