@@ -185,7 +185,7 @@ typedef struct moe_ops_w4_shape {
  * MOE_ERR_INVALID: null or misaligned pointers, sizes below their range,
  * strides shorter than a row, ldx % 8, zeros with MXFP4, E != 1;
  * MOE_ERR_UNSUPPORTED: K % 128, K > 8192, N, ldx or ldo > 2^24, M > 2^23,
- * (M / 16 + E + 1) * (N / 16 + 1) >= 2^31, unknown format, group or type.
+ * (M / 16 + E + 1) * (N / 16 + 1) >= 2^30, unknown format, group or type.
  */
 int moe_ops_w4_linear(const void* x_dev, const uint8_t* w_dev, const void* scales_dev,
                       const uint8_t* zeros_dev, const void* bias_dev,

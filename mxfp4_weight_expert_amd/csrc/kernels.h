@@ -131,6 +131,8 @@ struct CombineArgs {
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
 hipError_t launch_combine_backward(const CombineArgs& a, hipStream_t st);
 
+// Tasks (row tiles x weight sets) a 4-bit product may have.
+constexpr int64_t kW4MaxItems = int64_t{1} << 30;
 struct W4Args {
   const void* x;           // [M, K], rows ldx apart
   const int32_t* offsets;  // [E + 1] (grouped) or null

@@ -106,7 +106,7 @@ int check_w4(const moe_ops_w4_shape* s) {
   if (!known_dtype(s->out_dtype)) return MOE_ERR_UNSUPPORTED;
   // work items (row tiles x weight sets) are counted in 32 bits
   if ((static_cast<int64_t>(s->M) / 16 + s->E + 1) * (static_cast<int64_t>(s->N) / 16 + 1) >=
-      (int64_t{1} << 31))
+      kW4MaxItems)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -1,5 +1,3 @@
-#pragma once
-
 // Products of a few rows with 4-bit weights in the packed layout, for one
 // matrix or one per expert:
 //   out[m, n] = bias[n] + sum over groups g of s[n, g] *
@@ -22,6 +20,8 @@
 // The zero points are taken off as sum over g of (s z)[n, g] X[m, g], X the sum
 // of x over the group, by one 16x16x4 float MFMA a step: exact codes and one
 // correction in 32 bits.
+#pragma once
+
 #include "rows.h"
 #include "kernels.h"
 
@@ -32,8 +32,6 @@
 namespace moe {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 
 // 16-byte buffer load of weights, non-temporal (cache-policy operand 2) where
@@ -238,7 +236,9 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
     __syncthreads();
     tiles = __builtin_amdgcn_readfirstlane(tiles);
   }
-  const int items = tiles * ntn;
+  // the launcher's bound, which offsets that decrease could pass: the loop below
+  // must end without its index wrapping
+  const int items = static_cast<int>(min(static_cast<int64_t>(tiles) * ntn, kW4MaxItems));
 
   const uint32_t xrow = static_cast<uint32_t>(a.ldx) * 2;
   const uint32_t gbytes = static_cast<uint32_t>(nk) * kPkBlock;  // a weight group's
@@ -336,9 +336,11 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
         // Tokens through the wave's own LDS tile: loaded whole rows a KB at a
         // time, read as the MFMAs want them. Piece c of row m lies at c ^ m, so
         // the sixteen rows' pieces fall on different banks. Lanes of rows that
-        // were not loaded read one that was: their results are not stored.
+        // were not loaded read one that was: their results are not stored. INT4:
+        // the tokens in the order of the decoded codes.
 #pragma unroll
-        for (int i = 0; i < XL; ++i) *reinterpret_cast<uint4*>(s_tok + xlds[i]) = xg[d][i];
+        for (int i = 0; i < XL; ++i)
+          *reinterpret_cast<uint4*>(s_tok + xlds[i]) = kInt ? even_odd(xg[d][i]) : xg[d][i];
         __builtin_amdgcn_wave_barrier();
         uint4 xf[TT][4];
         float xs[TT];  // lane (m, q): of the sum of row m's tokens, INT4
@@ -359,7 +361,6 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
             for (int j = 0; j < 4; ++j) {
               if (j % kPer == 0) sum[j / kPer] = f32x4_t{0.f, 0.f, 0.f, 0.f};
               sum[j / kPer] = mfma_rows<DT>(uint4{one, one, one, one}, xf[t][j], sum[j / kPer]);
-              xf[t][j] = even_odd(xf[t][j]);
             }
             xs[t] = sum[0][0];
 #pragma unroll

@@ -355,6 +355,19 @@ def test_scales_that_are_no_numbers_stay_in_their_weight_row(dtype):
     assert not got[:, 7].any()
 
 
+@pytest.mark.parametrize("dtype,step", [("fp16", 2.0 ** -24), ("bf16", 2.0 ** -133)])
+def test_subnormal_tokens_count(dtype, step):
+    # tokens of 0 to 3 of the type's smallest steps: every sum is exact in 32 bits
+    K, N, M = 256, 20, 5
+    rng = np.random.default_rng(6)
+    x = torch.from_numpy(rng.integers(0, 4, size=(M, K)) * step).to(TORCH[dtype]).cuda()
+    scale = 2.0 ** 10
+    m, (W, _) = _matrix(rng, 1, N, K, "int4", 128, dtype, True, np.full((1, N, K // 128), scale))
+    shape = moe.W4Shape(M=M, N=N, K=K, format="int4", group=128, dtype=dtype, out_dtype="fp32")
+    got = moe.w4_linear(x, m["w"], m["scales"], shape, zeros=m["zeros"])
+    assert np.array_equal(f64(got), f64(x) @ W[0].T)
+
+
 def test_rows_of_x_do_not_meet():
     # a row of infinities and one of NaN: the others are as without them
     M, N, K = 20, 50, 1024

@@ -158,6 +158,7 @@ def _w4(shape, grouped=False, ldx=0, ldo=0, **kw):
     (dict(K=8192 + 128), 2), (dict(N=(1 << 24) + 1), 2), (dict(M=(1 << 23) + 1), 2), (dict(E=2049), 2),
     (dict(group=64), 2), (dict(format="int4", group=256), 2), (dict(format="int4", group=16), 2),
     (dict(dtype="fp32"), 2), (dict(M=1 << 23, N=1 << 24), 2),
+    (dict(M=1 << 20, N=1 << 18), 2),
 ])
 def test_w4_refuses_shapes(kw, code):
     assert _w4(_ws(**kw), grouped=True) == code
