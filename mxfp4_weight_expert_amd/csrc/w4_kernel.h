@@ -18,8 +18,8 @@
 // INT4 codes 0..15 are read as E4M3: its codes 0..15 are k * 2^-9 (subnormals
 // and the first binade), so the convert with scale 2^9 gives the code exactly.
 // The zero points are taken off as sum over g of (s z)[n, g] X[m, g], X the sum
-// of x over the group, by one 16x16x4 float MFMA a step: exact codes and one
-// correction in 32 bits.
+// of x over the group, by 16x16x4 float MFMAs: exact codes and one correction in
+// 32 bits.
 #pragma once
 
 #include "rows.h"
@@ -332,7 +332,15 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
       for (int d = 0; d < D; ++d) load(d, d);
       __syncthreads();  // scales are in LDS
 
-      auto compute = [&](int d, int ks) {
+      // INT4, lane (m, q): its share of the sums of row m's tokens that the zero
+      // points meet, and the place of the scale and zero point of weight row n = m.
+      // Groups of 64 and 128 leave half of the correction's four places free: it
+      // takes two steps at once (kPair), the first in lanes q < 2 (64 of 256 experts,
+      // K 7168, N 4096, groups of 64: 188 us step by step, 179 so).
+      constexpr bool kPair = kInt && G >= 64 && D == 2;
+      float xs[TT];
+      int zplace = 0;
+      auto compute = [&](int d, int ks, bool last) {
         // Tokens through the wave's own LDS tile: loaded whole rows a KB at a
         // time, read as the MFMAs want them. Piece c of row m lies at c ^ m, so
         // the sixteen rows' pieces fall on different banks. Lanes of rows that
@@ -343,7 +351,6 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
           *reinterpret_cast<uint4*>(s_tok + xlds[i]) = kInt ? even_odd(xg[d][i]) : xg[d][i];
         __builtin_amdgcn_wave_barrier();
         uint4 xf[TT][4];
-        float xs[TT];  // lane (m, q): of the sum of row m's tokens, INT4
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const uint32_t m = XL < 4 ? r & (4 * XL - 1) : t * 16 + r;
@@ -362,13 +369,22 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
               if (j % kPer == 0) sum[j / kPer] = f32x4_t{0.f, 0.f, 0.f, 0.f};
               sum[j / kPer] = mfma_rows<DT>(uint4{one, one, one, one}, xf[t][j], sum[j / kPer]);
             }
-            xs[t] = sum[0][0];
+            if constexpr (kPair) {
+              const float own = G == 64 ? (q & 1 ? sum[kGroups - 1][0] : sum[0][0]) : 0.5f * sum[0][0];
+              xs[t] = d == 0 ? (q < 2 ? own : 0.0f) : (q < 2 ? xs[t] : own);
+            } else {
+              xs[t] = sum[0][0];
 #pragma unroll
-            for (int g = 1; g < kGroups; ++g) xs[t] = q / kPer == g ? sum[g][0] : xs[t];
-            xs[t] *= 1.0f / kPer;  // the group's kPer lanes add up to it
+              for (int g = 1; g < kGroups; ++g) xs[t] = q / kPer == g ? sum[g][0] : xs[t];
+              xs[t] *= 1.0f / kPer;  // the group's kPer lanes add up to it
+            }
           }
         }
         __builtin_amdgcn_wave_barrier();
+        if constexpr (kPair) {
+          const int here = ks * kGroups + (G == 64 ? q & 1 : 0);
+          zplace = d == 0 || q >= 2 ? here : zplace;
+        }
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           const int wr = (set * RB + b) * 16 + r;  // weight row in the block's
@@ -416,7 +432,15 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
                 }
               }
             }
-            if constexpr (kInt) {
+            if constexpr (kPair) {
+              if (d == 1 || last) {
+                const float sz = scale16<DT>(*reinterpret_cast<const uint16_t*>(s_scale + wr * srow + 2 * zplace)) *
+                                 (a.zeros != nullptr ? static_cast<float>(s_zero[wr * zrow + zplace]) : 8.0f);
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                  acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xs[t], -sz, acc[b][t], 0, 0, 0);
+              }
+            } else if constexpr (kInt) {
               const int gq = q / kPer;
               float z = 8.0f, sq = s[0];
               if (a.zeros != nullptr) z = static_cast<float>(s_zero[wr * zrow + ks * kGroups + gq]);
@@ -433,7 +457,7 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
       for (int s0 = 0; s0 < nsteps; s0 += D) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-          if (s0 + d < nsteps) compute(d, k0 + place(s0 + d));
+          if (s0 + d < nsteps) compute(d, k0 + place(s0 + d), s0 + d + 1 >= nsteps);
           __builtin_amdgcn_sched_barrier(0);
           load(d, s0 + d + D);
           __builtin_amdgcn_sched_barrier(0);
@@ -521,6 +545,9 @@ void w4_go(const W4Args& a, hipStream_t st) {
   const int lds = w4_token_bytes<MT, W>() + ((nrow * groups * (kInt ? 2 : 1) + 15) & ~15) +
                   (kInt && a.zeros != nullptr ? (nrow * groups + 15) & ~15 : 0);
   auto kernel = w4_kernel<FMT, G, DT, MT, RB, W>;
+  // as many blocks as are resident, each with tasks in turn: twice to sixteen times
+  // as many were 0 to 14 % slower with experts and no faster with one matrix, and
+  // only as many as share the tasks evenly 4 to 8 % slower
   const int64_t most = int64_t{256} * w4_resident(kernel, 64 * W, lds);
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(64 * W), lds,
                      st, a);
