@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 from . import MOE_OK, MoeError, load_library
 
@@ -42,12 +42,19 @@ def _torch_dtype(name: str):
     return getattr(torch, _TORCH_NAME[name])
 
 
+class _Kept:
+    """A shape is copied and pickled by its fields, without what it keeps."""
+
+    def __reduce__(self):
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
+
+
 # A shape's C struct, torch types and array shapes are worked out at its first
 # call and kept on it: a decode step's calls are shorter than making them anew.
 
 
 @dataclass(frozen=True)
-class DispatchShape:
+class DispatchShape(_Kept):
     """Shape of dispatch and combine (fields as in moe_ops_dispatch_shape)."""
 
     T: int
@@ -80,7 +87,7 @@ class DispatchShape:
 
 
 @dataclass(frozen=True)
-class W4Shape:
+class W4Shape(_Kept):
     """Shape of the 4-bit products (fields as in moe_ops_w4_shape; the row
     strides come from the tensors). out_dtype None: dtype."""
 

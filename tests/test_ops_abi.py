@@ -190,6 +190,18 @@ def test_w4_refuses_before_launch():
     assert ops._entry("w4_linear")(None, None, None, None, None, None, None, None) == 1
 
 
+def test_shapes_copy_and_pickle_after_use():
+    import copy
+    import pickle
+
+    d, w = _ds(T=3), _ws(format="int4", group=64)
+    moe.dispatch_query(d)
+    assert w._c is not None and w._arrays  # what a call keeps on the shape
+    for s in (d, w):
+        for t in (copy.deepcopy(s), pickle.loads(pickle.dumps(s))):
+            assert t == s and hash(t) == hash(s)
+
+
 def test_binding_refuses_host_tensors_and_wrong_layouts():
     s = _ds(T=2, E=4, topk=2, H=8)
     x, ids = torch.zeros(2, 8, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32)
