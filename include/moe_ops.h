@@ -22,7 +22,8 @@
  * come before anything is enqueued. `stream` is a hipStream_t of the current
  * device (NULL: its default stream); the pointers must be usable there.
  * Outputs must not overlap inputs or each other (MOE_ERR_INVALID where the
- * ranges of large arrays show it). Nothing is kept between calls.
+ * ranges of large arrays show it). Nothing of a call is kept for the next;
+ * the products keep how many blocks of a kernel a GPU holds.
  */
 #ifndef MOE_OPS_H
 #define MOE_OPS_H

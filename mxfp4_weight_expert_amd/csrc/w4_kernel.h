@@ -519,19 +519,28 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
   }
 }
 
-// Blocks of a kernel that a CU holds, by its LDS (kept per size and instance).
-template <class F>
-int w4_resident(F kernel, int threads, int lds) {
-  static std::atomic<int> kept[161];
-  std::atomic<int>& k = kept[lds >> 10];
-  int n = k.load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(kernel), threads,
-                                                     (lds | 1023) + 1) != hipSuccess || n < 1)
-      n = 1;
-    k.store(n, std::memory_order_relaxed);
+// Blocks of a kernel that the current GPU holds at once, by its LDS; 0 where the
+// runtime does not say. Kept for each kernel, GPU and KB of LDS: asking takes longer
+// than a small launch. The kernel is the template's argument itself: instances have
+// one type between them, and would share what is kept for a type.
+template <auto Kernel>
+int w4_resident(int threads, int lds) {
+  constexpr int kGpus = 16;
+  static std::atomic<int> kept[kGpus][161];
+  int gpu = 0, per_cu = 0, cus = 0;
+  if (hipGetDevice(&gpu) == hipSuccess) {
+    std::atomic<int>* const k = gpu < kGpus ? &kept[gpu][lds >> 10] : nullptr;
+    if (k != nullptr && k->load(std::memory_order_relaxed) > 0) return k->load(std::memory_order_relaxed);
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, reinterpret_cast<const void*>(Kernel), threads,
+                                                     (lds | 1023) + 1) == hipSuccess &&
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, gpu) == hipSuccess &&
+        per_cu > 0 && cus > 0) {
+      if (k != nullptr) k->store(per_cu * cus, std::memory_order_relaxed);
+      return per_cu * cus;
+    }
   }
-  return n;
+  (void)hipGetLastError();  // a query's error is not the launch's
+  return 0;
 }
 
 template <int FMT, int G, int DT, int MT, int RB, int W>
@@ -544,11 +553,12 @@ void w4_go(const W4Args& a, hipStream_t st) {
   const int groups = (a.K >> 7) * (128 / G), nrow = RB * static_cast<int>(sets) * 16;
   const int lds = w4_token_bytes<MT, W>() + ((nrow * groups * (kInt ? 2 : 1) + 15) & ~15) +
                   (kInt && a.zeros != nullptr ? (nrow * groups + 15) & ~15 : 0);
-  auto kernel = w4_kernel<FMT, G, DT, MT, RB, W>;
+  constexpr auto kernel = w4_kernel<FMT, G, DT, MT, RB, W>;
   // as many blocks as are resident, each with tasks in turn: twice to sixteen times
   // as many were 0 to 14 % slower with experts and no faster with one matrix, and
   // only as many as share the tasks evenly 4 to 8 % slower
-  const int64_t most = int64_t{256} * w4_resident(kernel, 64 * W, lds);
+  const int resident = w4_resident<kernel>(64 * W, lds);
+  const int64_t most = resident > 0 ? resident : 256;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(64 * W), lds,
                      st, a);
 }
