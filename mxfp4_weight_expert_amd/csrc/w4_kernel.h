@@ -519,46 +519,85 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
   }
 }
 
-// Blocks of a kernel that the current GPU holds at once, by its LDS; 0 where the
-// runtime does not say. Kept for each kernel, GPU and KB of LDS: asking takes longer
-// than a small launch. The kernel is the template's argument itself: instances have
-// one type between them, and would share what is kept for a type.
+// CUs of the current GPU and blocks of a kernel that one of them holds, by the
+// block's LDS; blocks 0 where the runtime does not say. Kept for each kernel, GPU and
+// KB of LDS: asking takes longer than a small launch. The kernel is the template's
+// argument itself: instances have one type between them, and would share what is kept
+// for a type.
+struct W4Room {
+  int cus, blocks;
+};
 template <auto Kernel>
-int w4_resident(int threads, int lds) {
+W4Room w4_room(int threads, int lds) {
   constexpr int kGpus = 16;
-  static std::atomic<int> kept[kGpus][161];
-  int gpu = 0, per_cu = 0, cus = 0;
+  static std::atomic<int> kept[kGpus][161];  // cus << 8 | blocks
+  int gpu = 0, blocks = 0, cus = 0;
   if (hipGetDevice(&gpu) == hipSuccess) {
     std::atomic<int>* const k = gpu < kGpus ? &kept[gpu][lds >> 10] : nullptr;
-    if (k != nullptr && k->load(std::memory_order_relaxed) > 0) return k->load(std::memory_order_relaxed);
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, reinterpret_cast<const void*>(Kernel), threads,
+    const int v = k != nullptr ? k->load(std::memory_order_relaxed) : 0;
+    if (v > 0) return {v >> 8, v & 255};
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, reinterpret_cast<const void*>(Kernel), threads,
                                                      (lds | 1023) + 1) == hipSuccess &&
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, gpu) == hipSuccess &&
-        per_cu > 0 && cus > 0) {
-      if (k != nullptr) k->store(per_cu * cus, std::memory_order_relaxed);
-      return per_cu * cus;
+        blocks > 0 && cus > 0) {
+      if (k != nullptr) k->store(cus << 8 | blocks, std::memory_order_relaxed);
+      return {cus, blocks};
     }
   }
   (void)hipGetLastError();  // a query's error is not the launch's
-  return 0;
+  return {256, 0};
 }
 
-template <int FMT, int G, int DT, int MT, int RB, int W>
-void w4_go(const W4Args& a, hipStream_t st) {
+// LDS of a block that splits K over kw waves, without the kernel's static tables.
+template <int FMT, int G, int MT, int RB, int W>
+int w4_lds(const W4Args& a, int kw) {
   constexpr bool kInt = FMT == MOE_W4_INT4;
+  const int groups = (a.K >> 7) * (128 / G), nrow = RB * (W / kw) * 16;
+  return w4_token_bytes<MT, W>() + ((nrow * groups * (kInt ? 2 : 1) + 15) & ~15) +
+         (kInt && a.zeros != nullptr ? (nrow * groups + 15) & ~15 : 0);
+}
+constexpr int kW4MostLds = 150 << 10;   // of a CU's 160 KB, with room for the static tables
+constexpr int kW4WholeLds = 52 << 10;   // kw = 1 with 16-row tiles: 16 KB of tokens, 36 of scales
+
+// U: the 16-row weight groups that can be read (kw: see w4_rows).
+template <int FMT, int G, int DT, int MT, int RB, int W>
+void w4_go(const W4Args& a0, int64_t U, hipStream_t st) {
+  constexpr auto kernel = w4_kernel<FMT, G, DT, MT, RB, W>;
+  [[maybe_unused]] constexpr bool kInt = FMT == MOE_W4_INT4;
+  W4Args a = a0;
+  a.kw = W;
+  int lds = w4_lds<FMT, G, MT, RB, W>(a, W);
+  W4Room room = w4_room<kernel>(64 * W, lds);
+  if (W == 4 && U >= 2048) {
+    const int lds1 = w4_lds<FMT, G, MT, RB, W>(a, 1), nk = a.K >> 7;
+    bool whole = false;
+    if constexpr (MT == 1) {
+      const int64_t blocks = int64_t{room.cus} * std::max(room.blocks, 1);
+      const auto cost = [&](int64_t tasks, int steps) { return (tasks + blocks - 1) / blocks * (steps + 4); };
+      whole = lds1 <= kW4WholeLds && cost(U / (W * RB), nk) <= cost(U / RB, (nk + W - 1) / W);
+    } else if (lds1 <= kW4MostLds) {
+      const int64_t m = a.offsets != nullptr ? a.M / a.E : a.M, tiles = (m + 16 * MT - 1) / (16 * MT);
+      const auto cost = [&](int64_t tasks, int steps, int blocks) {
+        const int64_t each = (tasks + room.cus - 1) / room.cus;
+        return each * (2 * steps + (MT == 2 ? 5 : 4)) * (each > 1 && blocks > 1 ? 6 : kInt ? 10 : 8);
+      };
+      whole = cost(U * tiles / (W * RB), nk, w4_room<kernel>(64 * W, lds1).blocks) <
+              cost(U * tiles / RB, (nk + W - 1) / W, room.blocks);
+    }
+    if (whole) {
+      a.kw = 1;
+      lds = lds1;
+      room = w4_room<kernel>(64 * W, lds);
+    }
+  }
   const int64_t sets = W / a.kw;
   const int64_t ntn = ((a.N + 15) / 16 + RB * sets - 1) / (RB * sets);
   const int64_t tiles = (a.M + 16 * MT - 1) / (16 * MT) + (a.offsets != nullptr ? a.E : 0);
   const int64_t items = ntn * tiles;
-  const int groups = (a.K >> 7) * (128 / G), nrow = RB * static_cast<int>(sets) * 16;
-  const int lds = w4_token_bytes<MT, W>() + ((nrow * groups * (kInt ? 2 : 1) + 15) & ~15) +
-                  (kInt && a.zeros != nullptr ? (nrow * groups + 15) & ~15 : 0);
-  constexpr auto kernel = w4_kernel<FMT, G, DT, MT, RB, W>;
   // as many blocks as are resident, each with tasks in turn: twice to sixteen times
   // as many were 0 to 14 % slower with experts and no faster with one matrix, and
   // only as many as share the tasks evenly 4 to 8 % slower
-  const int resident = w4_resident<kernel>(64 * W, lds);
-  const int64_t most = resident > 0 ? resident : 256;
+  const int64_t most = int64_t{room.cus} * std::max(room.blocks, 1);
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(64 * W), lds,
                      st, a);
 }
@@ -566,11 +605,23 @@ void w4_go(const W4Args& a, hipStream_t st) {
 // The variant of a shape. U is the number of 16-row weight groups that can be
 // read (an expert without rows reads none), nk the K steps.
 //
-// - Many groups (U >= 2048): RB = 4, whose loads of tokens serve four groups.
-//   kw = 1 reads a group's whole K in one wave, with no join, but takes tasks four
-//   times as long: chosen where rounds of resident blocks times (steps + 4), the 4
-//   for a task's start and end, come out lower. K 384 x N 3584 of 896 experts:
-//   98 us against 204 with kw = 4; K 7168 x N 4096 of 64 experts: 166 against 135.
+// - Many groups (U >= 2048): RB = 4 with 16-row tiles, whose loads of tokens serve
+//   four groups, 2 with 32 and 64 rows. kw = 1 reads a group's whole K in one wave,
+//   with no join, but takes tasks four times as long, and four times the scales in
+//   LDS. It is chosen where its estimate is not the higher one:
+//   16-row tiles (the weights' stream bounds them): rounds of resident blocks (three a
+//   CU) times (steps + 4), the 4 for a task's start and end. K 384 x N 3584 of 896
+//   experts: 98 us against 204 with kw = 4; K 7168 x N 4096 of 64 experts: 166 against
+//   135. Up to 30 KB of scales a block leave room for three with kw = 1 too; from there
+//   to the limit of 36 two fit, which costs MXFP4 little (K 4096: N 2816 of 60 experts
+//   137 against 138, N 768 of 448 138 against 128) and INT4 nothing (groups of 64 with
+//   zero points, K 2560: N 768 of 896 experts 173 against 197).
+//   32 and 64 rows (decode, MFMAs and LDS bound them, so what the busiest CU has to do
+//   counts): tasks a CU times (steps + 2.5 or 2), and where a CU has one block at a
+//   time, which leaves its waits open, a third more with MXFP4, two with INT4. N 129279, 64 rows: K 1024 47 us with kw = 1, 71 with 4; INT4 of 64
+//   with zero points at K 2048 148 and 125, at K 4096 258 and 203, since kw = 1 leaves
+//   room for one block; N 65536, K 4096, 32 rows 46 and 51; 16 experts of 256 rows,
+//   K 3584, N 4096 362 and 312.
 // - Fewer: RB = 2, or 1 up to a group a CU, and K over eight waves from 16 steps on.
 //   8192 x 8192, 1 and 16 tokens: 9.3 and 12.3 us with RB = 2 and eight waves, 9.7
 //   and 15.3 with RB = 1, 13.4 and 15.6 with RB = 4 and four waves. 4096 x 4096:
@@ -585,42 +636,30 @@ void w4_go(const W4Args& a, hipStream_t st) {
 // M / E says many: K 2048 x N 4096, a quarter of 256 experts, M / E = 64 with 16
 // rows each, 84 us in tiles of 16, 133 in tiles of 64; M / E = 1024 with 256 rows
 // each (K 3584, N 768, 16 experts) 113 and 76.
-constexpr int kW4Kw1Scales = 36 << 10;  // with 16 KB of tokens, three blocks in a CU's LDS
 template <int FMT, int G, int DT>
-void w4_rows(const W4Args& a0, hipStream_t st) {
-  W4Args a = a0;
+void w4_rows(const W4Args& a, hipStream_t st) {
   constexpr bool kWide = !(FMT == MOE_W4_INT4 && G == 32);
   const bool grouped = a.offsets != nullptr;
   int mt = grouped ? (a.M / a.E > 128 ? 4 : 1) : a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
   if (mt == 4 && !kWide) mt = 1;
   const int64_t U = static_cast<int64_t>((a.N + 15) / 16) * (grouped ? std::min(a.E, a.M) : 1);
   const int nk = a.K >> 7;
-  a.kw = 4;
-  // scale rows (and zero points) of a kw = 1 block's RB * 64 weight rows in LDS
-  const int scales = (mt > 1 ? 128 : 256) * nk * (128 / G) *
-                     (a.format == MOE_W4_MXFP4 ? 1 : a.zeros != nullptr ? 3 : 2);
-  if (U >= 2048 && scales <= kW4Kw1Scales) {
-    constexpr int64_t kBlocks = 256 * 3;  // resident, as a rule
-    const auto cost = [&](int64_t tasks, int steps) { return (tasks + kBlocks - 1) / kBlocks * (steps + 4); };
-    if (cost(U / 16, nk) <= cost(U / 4, (nk + 3) / 4)) a.kw = 1;
-  }
   if (mt == 4) {
     if constexpr (kWide) {
-      if (U >= 512) w4_go<FMT, G, DT, 4, 2, 4>(a, st);
-      else w4_go<FMT, G, DT, 4, 1, 4>(a, st);
+      if (U >= 512) w4_go<FMT, G, DT, 4, 2, 4>(a, U, st);
+      else w4_go<FMT, G, DT, 4, 1, 4>(a, U, st);
     }
   } else if (mt == 2) {
-    if (U >= 512) w4_go<FMT, G, DT, 2, 2, 4>(a, st);
-    else w4_go<FMT, G, DT, 2, 1, 4>(a, st);
+    if (U >= 512) w4_go<FMT, G, DT, 2, 2, 4>(a, U, st);
+    else w4_go<FMT, G, DT, 2, 1, 4>(a, U, st);
   } else if (U >= 2048) {
-    w4_go<FMT, G, DT, 1, 4, 4>(a, st);
+    w4_go<FMT, G, DT, 1, 4, 4>(a, U, st);
   } else if (U > 512 || nk < 16) {
-    if (U > 256) w4_go<FMT, G, DT, 1, 2, 4>(a, st);
-    else w4_go<FMT, G, DT, 1, 1, 4>(a, st);
+    if (U > 256) w4_go<FMT, G, DT, 1, 2, 4>(a, U, st);
+    else w4_go<FMT, G, DT, 1, 1, 4>(a, U, st);
   } else {
-    a.kw = 8;
-    if (U > 256) w4_go<FMT, G, DT, 1, 2, 8>(a, st);
-    else w4_go<FMT, G, DT, 1, 1, 8>(a, st);
+    if (U > 256) w4_go<FMT, G, DT, 1, 2, 8>(a, U, st);
+    else w4_go<FMT, G, DT, 1, 1, 8>(a, U, st);
   }
 }
 

@@ -68,3 +68,12 @@ def test_launch_does_not_depend_on_products_that_ran_before():
         alone = _child(f"print(launches({second}))")
         after = _child(f"{first}()\nprint(launches({second}))")
         assert after == alone
+
+
+def test_tiles_of_64_rows_leave_room_for_two_blocks():
+    # 64 KB of tokens a block: with a wave reading all of K, the scales of 128 weight
+    # rows (24 KB here) keep a second block off the CU, where a fourth of them does not
+    call = 'w4(64, 129279, 4096, format="int4", group=64)'
+    print(f"[ops] launch of {call}", flush=True)
+    (_, threads, lds), = eval(_child(f"print(launches({call}))"))
+    assert threads == 256 and 2 * (lds + 8224) <= 160 << 10  # 8224: the table of experts' tiles
