@@ -153,6 +153,10 @@ int moe_ops_combine_backward(const void* dout_dev, const void* rows_dev,
  * which is exact too: scale bytes up to 252 (then no weight passes the
  * type's range; bytes 253 and 254 may give infinities). INT4 zero points come
  * off a group's sum, so an infinite x gives NaN there.
+ *
+ * Deterministic. For one shape a row's result depends, to the bit, on the row and
+ * its matrix alone: not on its place in x, nor on the other rows and their experts.
+ * Another shape (M among its fields) may sum in another order.
  */
 typedef struct moe_ops_w4_shape {
   int32_t M;

@@ -316,8 +316,10 @@ __global__ __launch_bounds__(64 * W, MT == 1 && W == 4 ? 3 : 2) void w4_kernel(W
       }
       // The blocks of an XCD take a row tile's steps from different places on:
       // in step, all of them would ask one L2 channel for the same tokens, whose
-      // rows are often a multiple of the channels' span apart.
-      const int turn = ((item >> 3) + kpart * (nsteps >> 2)) % max(nsteps, 1);
+      // rows are often a multiple of the channels' span apart. The place goes by matrix
+      // and weight rows alone, so the order of a row's sums has nothing to do with where
+      // in the batch it lies.
+      const int turn = (((e * ntn + tn) >> 3) + kpart * (nsteps >> 2)) % max(nsteps, 1);
       auto place = [&](int step) { return step + turn < nsteps ? step + turn : step + turn - nsteps; };
       auto load = [&](int d, int step) {  // step: wave-uniform
         const bool in = step < nsteps;
@@ -635,7 +637,7 @@ void w4_go(const W4Args& a0, int64_t U, hipStream_t st) {
 // which counts those that live elsewhere too, so experts take tiles of 16 until
 // M / E says many: K 2048 x N 4096, a quarter of 256 experts, M / E = 64 with 16
 // rows each, 84 us in tiles of 16, 133 in tiles of 64; M / E = 1024 with 256 rows
-// each (K 3584, N 768, 16 experts) 113 and 76.
+// each (K 3584, N 768, 16 experts) 113 and 69.
 template <int FMT, int G, int DT>
 void w4_rows(const W4Args& a, hipStream_t st) {
   constexpr bool kWide = !(FMT == MOE_W4_INT4 && G == 32);
