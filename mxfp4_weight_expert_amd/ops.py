@@ -5,6 +5,10 @@ Argument checks and marshalling only; every step runs in the library's HIP
 kernels, on the current stream of the tensors' device or on `stream` (a raw
 stream handle of that device), which has to be ordered after the inputs' writers.
 Outputs and the workspace are allocated, for that stream, when not given.
+
+Nothing is recorded for autograd: a tensor that requires a gradient is refused
+where gradients are being recorded. The *_backward functions are the gradients,
+for a torch.autograd.Function whose forward and backward make these calls.
 """
 from __future__ import annotations
 
@@ -146,13 +150,16 @@ def _refuse(t, what: str, shape: tuple, dtype, index: int, layout: str):
     if t.get_device() != index:
         first = f"GPU {index}" if index >= 0 else "the CPU"
         raise ValueError(f"{what} is on {t.device}, the first tensor on {first}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, and this call would record none: make it under "
+                         "torch.no_grad() or in a torch.autograd.Function")
     raise ValueError(f"{what} must {layout}")
 
 
 def _check(t, what: str, shape: tuple, dtype, index: int) -> int:
     """A contiguous tensor's address. index: the GPU of the call's first tensor."""
     if (t.dtype is dtype and t.shape == shape and t.get_device() == index
-            and t.is_contiguous()):
+            and t.is_contiguous() and not (t.requires_grad and torch.is_grad_enabled())):
         return t.data_ptr()
     _refuse(t, what, shape, dtype, index, "be contiguous")
 
@@ -160,7 +167,8 @@ def _check(t, what: str, shape: tuple, dtype, index: int) -> int:
 def _row_stride(t, what: str, shape: tuple, dtype, index: int) -> int:
     """Elements between the rows of a matrix whose rows are contiguous; 0 where
     the rows follow each other."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and not (t.requires_grad and torch.is_grad_enabled())):
         if t.is_contiguous():
             return 0
         if (shape[1] <= 1 or t.stride(1) == 1) and (shape[0] <= 1 or t.stride(0) >= shape[1]):

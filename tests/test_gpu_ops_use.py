@@ -72,3 +72,75 @@ def test_a_rows_bits_do_not_depend_on_its_place(M, N, K, fmt, group):
     at = torch.from_numpy(rng.permutation(M)).cuda()
     want = moe.w4_linear(x, m["w"], m["scales"], shape)
     assert torch.equal(moe.w4_linear(x[at], m["w"], m["scales"], shape), want[at])
+
+
+# ------------------------------------------------------------------ autograd
+
+
+def _routed(T=6, topk=2, E=4, H=128, dtype=torch.bfloat16):
+    shape = moe.DispatchShape(T=T, E=E, topk=topk, H=H)
+    ids = torch.arange(T * topk, dtype=torch.int32, device="cuda").view(T, topk) % E
+    x = torch.randn(T, H, device="cuda").to(dtype)
+    rows, off, _, back = moe.dispatch(x, ids, shape)
+    return shape, ids, x, rows, off, back, torch.rand(T, topk, device="cuda")
+
+
+def test_tensors_that_require_gradients_are_refused():
+    shape, ids, x, rows, off, back, w = _routed()
+    s = moe.W4Shape(M=12, N=32, K=128, E=4)
+    c = torch.zeros(4, 32, 64, dtype=torch.uint8, device="cuda")
+    sc = torch.full((4, 32, 4), 127, dtype=torch.uint8, device="cuda")
+    bias = torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")
+    one = moe.W4Shape(M=12, N=32, K=128)
+
+    def want(t):
+        return t.detach().clone().requires_grad_()
+
+    calls = {
+        "x": [lambda: moe.dispatch(want(x), ids, shape),
+              lambda: moe.w4_linear(want(rows), c[:1], sc[:1], one),
+              lambda: moe.w4_grouped_linear(want(rows), off, c, sc, s)],
+        "rows": [lambda: moe.combine(want(rows), back, w, shape),
+                 lambda: moe.combine_backward(x, want(rows), back, w, shape)],
+        "topk_w": [lambda: moe.combine(rows, back, want(w), shape),
+                   lambda: moe.combine_backward(x, rows, back, want(w), shape)],
+        "dout": [lambda: moe.combine_backward(want(x), rows, back, w, shape)],
+        "drows": [lambda: moe.dispatch_backward(want(rows), back, shape)],
+        "bias": [lambda: moe.w4_grouped_linear(rows, off, c, sc, s, bias=want(bias))],
+        "out": [lambda: moe.combine(rows, back, w, shape, out=want(x)),
+                lambda: moe.w4_linear(rows, c[:1], sc[:1], one, out=want(bias.new_zeros(12, 32)))],
+    }
+    for name, fs in calls.items():
+        for f in fs:
+            with pytest.raises(ValueError, match=f"{name} requires a gradient"):
+                f()
+            with torch.no_grad():
+                f()  # where nothing is recorded, nothing is lost
+
+
+def test_operators_inside_an_autograd_function():
+    # forward and backward of a function run without recording: the operators take
+    # the tensors there, leaves that require gradients among the saved ones
+    shape, ids, x, _, _, _, w = _routed()
+
+    class Routed(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            rows, _, _, back = moe.dispatch(x, ids, shape)
+            ctx.save_for_backward(rows, back, w)
+            return moe.combine(rows, back, w, shape)
+
+        @staticmethod
+        def backward(ctx, dout):
+            rows, back, w = ctx.saved_tensors
+            drows, dw = moe.combine_backward(dout.contiguous(), rows, back, w, shape)
+            return moe.dispatch_backward(drows, back, shape), dw
+
+    xl, wl = x.clone().requires_grad_(), w.clone().requires_grad_()
+    Routed.apply(xl, wl).float().sum().backward()
+    # dout is 1: dx = sum_k w, each w rounded in its row of drows and the sum once more;
+    # dw is the sum of the token's row
+    sw = f64(w).sum(1, keepdims=True)
+    _close(xl.grad, np.broadcast_to(sw, x.shape), 2.01 * sw * 2.0 ** -8 + 2.0 ** -20, "dx")
+    ref = np.repeat(f64(x).sum(1)[:, None], 2, 1)
+    _close(wl.grad, ref, 20 * 2.0 ** -24 * np.abs(f64(x)).sum(1)[:, None], "dw")
