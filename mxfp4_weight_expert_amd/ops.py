@@ -8,7 +8,8 @@ Outputs and the workspace are allocated, for that stream, when not given.
 
 Nothing is recorded for autograd: a tensor that requires a gradient is refused
 where gradients are being recorded. The *_backward functions are the gradients,
-for a torch.autograd.Function whose forward and backward make these calls.
+for a torch.autograd.Function whose forward and backward make these calls. What a
+call writes counts as changed, so that autograd refuses values it had saved of it.
 """
 from __future__ import annotations
 
@@ -36,13 +37,15 @@ class _W4Shape(ctypes.Structure):
                                                                ("ldo", ctypes.c_int64)]
 
 
-torch = None  # imported by the first call: the binding itself needs none
+# imported by the first call: the binding itself needs none
+torch = _changed = None
 
 
 def _torch_dtype(name: str):
-    global torch
+    global torch, _changed
     import torch
 
+    _changed = torch._C._increment_version  # torch.autograd.graph.increment_version, of tuples
     return getattr(torch, _TORCH_NAME[name])
 
 
@@ -243,6 +246,7 @@ def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_s
          _check(row_slot, "row_slot", sorted_rows[:1], i32, gpu),
          _check(slot_row, "slot_row", maps, i32, gpu),
          _check(workspace, "workspace", workspace.shape, torch.uint8, gpu), workspace.numel())
+    _changed((out, offsets, row_slot, slot_row))
     return out, offsets, row_slot, slot_row
 
 
@@ -258,6 +262,7 @@ def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None, stream
     if out is None:
         out = torch.empty(tokens, dtype=dt, device=drows.device)
     _run("dispatch_backward", gpu, pd, ps, shape._c, _check(out, "out", tokens, dt, gpu))
+    _changed((out,))
     return out
 
 
@@ -277,6 +282,7 @@ def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None, stream=No
     if out is None:
         out = torch.empty(tokens, dtype=dt, device=rows.device)
     _run("combine", gpu, pr, ps, pw, shape._c, _check(out, "out", tokens, dt, gpu))
+    _changed((out,))
     return out
 
 
@@ -299,6 +305,7 @@ def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=N
         dw = torch.empty(maps, dtype=f32, device=dout.device)
     _run("combine_backward", gpu, pd, pr, ps, pw, shape._c, _check(dy, "dy", sorted_rows, dt, gpu),
          _check(dw, "dw", maps, f32, gpu))
+    _changed((dy, dw))
     return dy, dw
 
 
@@ -326,6 +333,7 @@ def _w4(name, x, offsets, w, scales, shape, zeros, bias, out):
     if grouped:
         args = (_check(offsets, "offsets", (shape.E + 1,), torch.int32, gpu), *args)
     _run(name, gpu, x.data_ptr(), *args)
+    _changed((out,))
     return out
 
 

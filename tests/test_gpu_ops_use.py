@@ -144,3 +144,35 @@ def test_operators_inside_an_autograd_function():
     _close(xl.grad, np.broadcast_to(sw, x.shape), 2.01 * sw * 2.0 ** -8 + 2.0 ** -20, "dx")
     ref = np.repeat(f64(x).sum(1)[:, None], 2, 1)
     _close(wl.grad, ref, 20 * 2.0 ** -24 * np.abs(f64(x)).sum(1)[:, None], "dw")
+
+
+def test_outputs_given_count_as_changed():
+    # a tensor that a recorded product saved, then given as an output: its old values
+    # are gone, and the gradient that needs them has to be refused
+    shape, ids, x, rows, off, back, w = _routed()
+    s, one = moe.W4Shape(M=12, N=128, K=128, E=4), moe.W4Shape(M=12, N=128, K=128)
+    c = torch.zeros(4, 128, 64, dtype=torch.uint8, device="cuda")
+    sc = torch.full((4, 128, 4), 127, dtype=torch.uint8, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    maps = dict(offsets=torch.zeros(5, **i32), row_slot=torch.zeros(12, **i32), slot_row=torch.zeros(6, 2, **i32))
+    before = [t._version for t in maps.values()]
+    moe.dispatch(x, ids, shape, **maps)
+    assert all(t._version > v for t, v in zip(maps.values(), before))
+    calls = [
+        (rows, lambda b: moe.dispatch(x, ids, shape, out=b)),
+        (x, lambda b: moe.combine(rows, back, w, shape, out=b)),
+        (x, lambda b: moe.dispatch_backward(rows, back, shape, out=b)),
+        (rows, lambda b: moe.combine_backward(x, rows, back, w, shape, dy=b)),
+        (w, lambda b: moe.combine_backward(x, rows, back, w, shape, dw=b)),
+        (rows, lambda b: moe.w4_linear(rows, c[:1], sc[:1], one, out=b)),
+        (rows, lambda b: moe.w4_grouped_linear(rows, off, c, sc, s, out=b)),
+    ]
+    for like, call in calls:
+        buf = torch.ones_like(like)
+        leaf = torch.ones_like(like).requires_grad_()
+        y = (leaf * buf).sum()
+        call(buf)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    with torch.inference_mode():  # tensors without a version
+        moe.combine(rows, back, w, shape, out=torch.zeros_like(x))
