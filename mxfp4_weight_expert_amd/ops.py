@@ -167,6 +167,13 @@ def _check(t, what: str, shape: tuple, dtype, index: int) -> int:
     _refuse(t, what, shape, dtype, index, "be contiguous")
 
 
+def _whole(t, what: str, shape: tuple, dtype, index: int) -> int:
+    """_check for whole numbers, which never require a gradient."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, what, shape, dtype, index, "be contiguous")
+
+
 def _row_stride(t, what: str, shape: tuple, dtype, index: int) -> int:
     """Elements between the rows of a matrix whose rows are contiguous; 0 where
     the rows follow each other."""
@@ -229,7 +236,7 @@ def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_s
                             slot_row=slot_row, workspace=workspace)
     tokens, sorted_rows, maps = shape._arrays
     gpu, i32 = x.get_device(), torch.int32
-    px, pi = _check(x, "x", tokens, dt, gpu), _check(topk_ids, "topk_ids", maps, i32, gpu)
+    px, pi = _check(x, "x", tokens, dt, gpu), _whole(topk_ids, "topk_ids", maps, i32, gpu)
     dev = x.device
     if out is None:
         out = torch.empty(sorted_rows, dtype=dt, device=dev)
@@ -242,10 +249,10 @@ def dispatch(x, topk_ids, shape: DispatchShape, *, out=None, offsets=None, row_s
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _run("dispatch", gpu, px, pi, shape._c, _check(out, "out", sorted_rows, dt, gpu),
-         _check(offsets, "offsets", (shape.E + 1,), i32, gpu),
-         _check(row_slot, "row_slot", sorted_rows[:1], i32, gpu),
-         _check(slot_row, "slot_row", maps, i32, gpu),
-         _check(workspace, "workspace", workspace.shape, torch.uint8, gpu), workspace.numel())
+         _whole(offsets, "offsets", (shape.E + 1,), i32, gpu),
+         _whole(row_slot, "row_slot", sorted_rows[:1], i32, gpu),
+         _whole(slot_row, "slot_row", maps, i32, gpu),
+         _whole(workspace, "workspace", workspace.shape, torch.uint8, gpu), workspace.numel())
     _changed((out, offsets, row_slot, slot_row))
     return out, offsets, row_slot, slot_row
 
@@ -258,7 +265,7 @@ def dispatch_backward(drows, slot_row, shape: DispatchShape, *, out=None, stream
             return dispatch_backward(drows, slot_row, shape, out=out)
     tokens, sorted_rows, maps = shape._arrays
     gpu = drows.get_device()
-    pd, ps = _check(drows, "drows", sorted_rows, dt, gpu), _check(slot_row, "slot_row", maps, torch.int32, gpu)
+    pd, ps = _check(drows, "drows", sorted_rows, dt, gpu), _whole(slot_row, "slot_row", maps, torch.int32, gpu)
     if out is None:
         out = torch.empty(tokens, dtype=dt, device=drows.device)
     _run("dispatch_backward", gpu, pd, ps, shape._c, _check(out, "out", tokens, dt, gpu))
@@ -277,7 +284,7 @@ def combine(rows, slot_row, topk_w, shape: DispatchShape, *, out=None, stream=No
             return combine(rows, slot_row, topk_w, shape, out=out)
     tokens, sorted_rows, maps = shape._arrays
     gpu = rows.get_device()
-    pr, ps = _check(rows, "rows", sorted_rows, dt, gpu), _check(slot_row, "slot_row", maps, torch.int32, gpu)
+    pr, ps = _check(rows, "rows", sorted_rows, dt, gpu), _whole(slot_row, "slot_row", maps, torch.int32, gpu)
     pw = _check(topk_w, "topk_w", maps, torch.float32, gpu)
     if out is None:
         out = torch.empty(tokens, dtype=dt, device=rows.device)
@@ -298,7 +305,7 @@ def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=N
     tokens, sorted_rows, maps = shape._arrays
     gpu, f32 = dout.get_device(), torch.float32
     pd, pr = _check(dout, "dout", tokens, dt, gpu), _check(rows, "rows", sorted_rows, dt, gpu)
-    ps, pw = _check(slot_row, "slot_row", maps, torch.int32, gpu), _check(topk_w, "topk_w", maps, f32, gpu)
+    ps, pw = _whole(slot_row, "slot_row", maps, torch.int32, gpu), _check(topk_w, "topk_w", maps, f32, gpu)
     if dy is None:
         dy = torch.empty(sorted_rows, dtype=dt, device=dout.device)
     if dw is None:
@@ -311,9 +318,8 @@ def combine_backward(dout, rows, slot_row, topk_w, shape: DispatchShape, *, dy=N
 
 def _matrix(t, what: str, bare: tuple, shape: tuple, dtype, gpu: int, grouped: bool):
     """Address of a matrix array; a single matrix may come without its leading 1."""
-    if t is None:
-        return None
-    return _check(t, what, shape if grouped or t.dim() == len(shape) else bare, dtype, gpu)
+    check = _whole if dtype is torch.uint8 else _check
+    return check(t, what, shape if grouped or t.dim() == len(shape) else bare, dtype, gpu)
 
 
 def _w4(name, x, offsets, w, scales, shape, zeros, bias, out):
@@ -328,10 +334,11 @@ def _w4(name, x, offsets, w, scales, shape, zeros, bias, out):
     cshape = ctypes.byref(shape.to_c(ldx, ldo)) if ldx or ldo else shape._c
     args = (_matrix(w, "w", one[0], every[0], torch.uint8, gpu, grouped),
             _matrix(scales, "scales", one[1], every[1], sdt, gpu, grouped),
-            _matrix(zeros, "zeros", one[1], every[1], torch.uint8, gpu, grouped),
-            _matrix(bias, "bias", one[2], every[2], dt, gpu, grouped), cshape, out.data_ptr())
+            None if zeros is None else _matrix(zeros, "zeros", one[1], every[1], torch.uint8, gpu, grouped),
+            None if bias is None else _matrix(bias, "bias", one[2], every[2], dt, gpu, grouped),
+            cshape, out.data_ptr())
     if grouped:
-        args = (_check(offsets, "offsets", (shape.E + 1,), torch.int32, gpu), *args)
+        args = (_whole(offsets, "offsets", (shape.E + 1,), torch.int32, gpu), *args)
     _run(name, gpu, x.data_ptr(), *args)
     _changed((out,))
     return out
