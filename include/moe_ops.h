@@ -21,9 +21,11 @@
  * returns MOE_OK or an MOE_ERR_* code of moe_mxfp4.h, and argument errors
  * come before anything is enqueued. `stream` is a hipStream_t of the current
  * device (NULL: its default stream); the pointers must be usable there.
- * Outputs must not overlap inputs or each other (MOE_ERR_INVALID where the
- * ranges of large arrays show it). Nothing of a call is kept for the next;
- * the products keep how many blocks of a kernel a GPU holds.
+ * Outputs must not overlap inputs or each other (MOE_ERR_INVALID where their
+ * ranges do; rows of the products' x and out that are the same number of bytes
+ * apart may lie between each other, as columns of one matrix). Nothing of a
+ * call is kept for the next; the products keep how many blocks of a kernel a
+ * GPU holds.
  */
 #ifndef MOE_OPS_H
 #define MOE_OPS_H

@@ -25,6 +25,18 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
          y < x + static_cast<uintptr_t>(na);
 }
 
+// Rows of two matrices, `rows` of each, na and nb bytes long and sa and sb apart. With
+// the same stride the rows of the one may lie between those of the other; with
+// different ones the ranges decide.
+bool rows_overlap(const void* a, int64_t na, int64_t sa, const void* b, int64_t nb, int64_t sb,
+                  int64_t rows) {
+  if (!overlap(a, (rows - 1) * sa + na, b, (rows - 1) * sb + nb)) return false;
+  if (sa != sb) return true;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t at = (d % sa + sa) % sa;  // from a row of a to the next row of b
+  return at < na || at + nb > sa;
+}
+
 int check(const moe_ops_dispatch_shape* s) {
   if (s == nullptr) return MOE_ERR_INVALID;
   if (s->T < 0 || s->E < 1 || s->topk < 1 || s->H < 1 || s->expert_offset < 0)
@@ -130,11 +142,11 @@ int w4_impl(const void* x, const int32_t* offsets, bool grouped, const uint8_t* 
       !aligned(offsets, 4))
     return MOE_ERR_INVALID;
   const int64_t ldx = s.ldx != 0 ? s.ldx : s.K, ldo = s.ldo != 0 ? s.ldo : s.N;
-  const int64_t nx = ((s.M - 1) * ldx + s.K) * 2;
-  const int64_t no = ((s.M - 1) * ldo + s.N) * size_of(s.out_dtype);
+  const int64_t osize = size_of(s.out_dtype), no = ((s.M - 1) * ldo + s.N) * osize;
   const int64_t np = (static_cast<int64_t>(s.N) + 15) / 16 * 16;
   const int64_t ngroup = static_cast<int64_t>(s.E) * s.N * (s.K / s.group);
-  if (overlap(out, no, x, nx) || overlap(out, no, w, s.E * np * (s.K / 2)) ||
+  if (rows_overlap(x, static_cast<int64_t>(s.K) * 2, ldx * 2, out, s.N * osize, ldo * osize, s.M) ||
+      overlap(out, no, w, s.E * np * (s.K / 2)) ||
       overlap(out, no, scales, ngroup * (s.format == MOE_W4_MXFP4 ? 1 : 2)) ||
       overlap(out, no, zeros, ngroup) || overlap(out, no, bias, static_cast<int64_t>(s.E) * s.N * 2) ||
       overlap(out, no, offsets, (static_cast<int64_t>(s.E) + 1) * 4))

@@ -176,3 +176,33 @@ def test_outputs_given_count_as_changed():
             y.backward()
     with torch.inference_mode():  # tensors without a version
         moe.combine(rows, back, w, shape, out=torch.zeros_like(x))
+
+
+# ------------------------------------------------------------------ memory
+
+
+@pytest.mark.parametrize("odt", ["bf16", "fp32"])
+def test_x_and_out_as_columns_of_one_matrix(odt):
+    # the rows of the one lie between the rows of the other, on either side
+    M, N, K = 37, 72, 256
+    rng = np.random.default_rng(12)
+    m, (W, mag) = _matrices(rng, 1, N, K)
+    size = 2 if odt == "bf16" else 4
+    width = K + N * size // 2 + 8
+    shape = moe.W4Shape(M=M, N=N, K=K, out_dtype=odt)
+    for xfirst in (True, False):
+        wide = torch.from_numpy(rng.standard_normal((M, width))).to(torch.bfloat16).cuda()
+        at = 0 if xfirst else N * size // 2
+        x = wide[:, at:at + K]
+        out = wide.view(TORCH[odt])[:, 2 * K // size:2 * K // size + N] if xfirst else wide.view(TORCH[odt])[:, :N]
+        keep, x0 = wide[:, at + K:] if not xfirst else wide[:, K + N * size // 2:], x.clone()
+        keep0 = keep.clone()
+        for grouped in (False, True):
+            if grouped:
+                _grouped(m, x, [0, M], shape, out=out)
+            else:
+                moe.w4_linear(x, m["w"], m["scales"], shape, out=out)
+            torch.cuda.synchronize()
+            assert torch.equal(x, x0) and torch.equal(keep, keep0)
+            ref, mags = f64(x) @ W[0].T, np.abs(f64(x)) @ mag[0].T
+            _close(out, ref, round_tol(ref, odt, sum_tol(K) * mags), f"x first {xfirst}, grouped {grouped}")

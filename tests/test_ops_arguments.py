@@ -1,8 +1,17 @@
 """Host-side checks of the operators' arguments (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
 import mxfp4_weight_expert_amd as moe
+from mxfp4_weight_expert_amd import ops
+
+# Fabricated addresses: never where a kernel could start.
+no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0,
+                            reason="fabricated device addresses: run only where no GPU is visible")
+GB = 1 << 30
+HIP = 4  # MOE_ERR_HIP: past every check, and no GPU to launch on
 
 
 def test_tensors_that_require_gradients_are_refused():
@@ -26,3 +35,27 @@ def test_tensors_that_require_gradients_are_refused():
                 f(lambda t: t.clone().requires_grad_())
             with torch.no_grad(), pytest.raises(ValueError, match="GPU"):
                 f(lambda t: t.clone().requires_grad_())  # goes on to the next check
+
+
+def _w4(x, out, M=5, N=48, K=128, ldx=0, ldo=0, out_dtype="bf16"):
+    c = moe.W4Shape(M=M, N=N, K=K, out_dtype=out_dtype).to_c(ldx, ldo)
+    p = [ctypes.c_void_p(v) if v else None for v in (x, 8 * GB, 9 * GB, 0, 0)]
+    return ops._entry("w4_linear")(*p, ctypes.byref(c), ctypes.c_void_p(out), None)
+
+
+@no_gpu
+def test_rows_of_out_between_rows_of_x():
+    x, ld = GB, 128 + 48 + 16  # elements of two bytes
+    for out in (x + 2 * 128, x + 2 * (128 + 16)):  # right behind a row of x, right before the next
+        assert _w4(x, out, ldx=ld, ldo=ld) == HIP
+    for out in (x + 2 * 127, x + 2 * (128 + 17), x, x - 2 * 47, x - 2 * 48 + 2):  # one element into a row
+        assert _w4(x, out, ldx=ld, ldo=ld) == 1
+    assert _w4(x, x - 2 * 48, ldx=ld, ldo=ld) == HIP  # before the first row, and between the others
+    assert _w4(x, x - 2 * (ld + 48), ldx=ld, ldo=ld) == HIP
+    # 32-bit results: the same bytes from row to row are half the elements
+    assert _w4(x, x + 2 * 128, N=24, ldx=ld, ldo=ld // 2, out_dtype="fp32") == HIP
+    assert _w4(x, x + 2 * 126, N=24, ldx=ld, ldo=ld // 2, out_dtype="fp32") == 1
+    # rows that drift against each other: refused, also where they should miss
+    assert _w4(x, x + 2 * 128, ldx=ld, ldo=ld + 8) == 1
+    assert _w4(x, x + 2 * (4 * ld + 128), ldx=ld, ldo=ld + 8) == HIP  # behind the last row
+    assert _w4(x, x + 2 * 128, M=1, ldx=ld, ldo=48) == HIP  # one row has no next
