@@ -89,7 +89,8 @@ int moe_ops_dispatch_query(const moe_ops_dispatch_shape* shape, uint64_t* worksp
  *
  * Deterministic. T = 0 writes zeros to offsets and reads nothing. Alignment:
  * rows their element size, maps 4 bytes, workspace 256 bytes.
- * MOE_ERR_WORKSPACE: workspace NULL, too small or misaligned. Calls that
+ * MOE_ERR_WORKSPACE: workspace NULL, too small or misaligned; MOE_ERR_INVALID:
+ * its first bytes, as many as are needed, on an input or output. Calls that
  * may overlap in time need workspaces of their own (two captured graphs that
  * can run at once among them).
  */

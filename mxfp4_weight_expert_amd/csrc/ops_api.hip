@@ -193,6 +193,15 @@ int moe_ops_dispatch(const void* x_dev, const int32_t* topk_ids_dev,
   const moe_ops_dispatch_shape& s = *shape;
   const uintptr_t al = static_cast<uintptr_t>(size_of(s.dtype));
   if (offsets_dev == nullptr || !aligned(offsets_dev, 4)) return MOE_ERR_INVALID;
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  const Extents n(s);
+  const Range in[2] = {{x_dev, n.tokens}, {topk_ids_dev, n.map}};
+  const Range out[4] = {{rows_dev, n.rows}, {offsets_dev, (static_cast<int64_t>(s.E) + 1) * 4},
+                        {row_slot_dev, n.map}, {slot_row_dev, n.map}};
+  const auto meet = [](const Range& a, const Range& b) { return overlap(a.p, a.bytes, b.p, b.bytes); };
   if (s.T > 0) {
     if (x_dev == nullptr || topk_ids_dev == nullptr || rows_dev == nullptr ||
         row_slot_dev == nullptr || slot_row_dev == nullptr)
@@ -200,24 +209,20 @@ int moe_ops_dispatch(const void* x_dev, const int32_t* topk_ids_dev,
     if (!aligned(x_dev, al) || !aligned(rows_dev, al) || !aligned(topk_ids_dev, 4) ||
         !aligned(row_slot_dev, 4) || !aligned(slot_row_dev, 4))
       return MOE_ERR_INVALID;
-    const Extents n(s);
-    const int64_t no = (static_cast<int64_t>(s.E) + 1) * 4;
-    struct Range {
-      const void* p;
-      int64_t bytes;
-    };
-    const Range out[4] = {{rows_dev, n.rows}, {offsets_dev, no}, {row_slot_dev, n.map}, {slot_row_dev, n.map}};
     for (int i = 0; i < 4; ++i) {
-      if (overlap(out[i].p, out[i].bytes, x_dev, n.tokens) ||
-          overlap(out[i].p, out[i].bytes, topk_ids_dev, n.map))
-        return MOE_ERR_INVALID;
+      if (meet(out[i], in[0]) || meet(out[i], in[1])) return MOE_ERR_INVALID;
       for (int j = 0; j < i; ++j)
-        if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return MOE_ERR_INVALID;
+        if (meet(out[i], out[j])) return MOE_ERR_INVALID;
     }
   }
   const DispatchWs ws = dispatch_ws(s);
   if (workspace_dev == nullptr || !aligned(workspace_dev, 256) || workspace_bytes < ws.bytes)
     return MOE_ERR_WORKSPACE;
+  const Range work = {workspace_dev, static_cast<int64_t>(ws.bytes)};
+  for (const Range& r : in)
+    if (meet(work, r)) return MOE_ERR_INVALID;
+  for (const Range& r : out)
+    if (meet(work, r)) return MOE_ERR_INVALID;
   DispatchArgs a{};
   a.x = static_cast<const uint8_t*>(x_dev);
   a.ids = topk_ids_dev;

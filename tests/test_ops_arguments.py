@@ -59,3 +59,24 @@ def test_rows_of_out_between_rows_of_x():
     assert _w4(x, x + 2 * 128, ldx=ld, ldo=ld + 8) == 1
     assert _w4(x, x + 2 * (4 * ld + 128), ldx=ld, ldo=ld + 8) == HIP  # behind the last row
     assert _w4(x, x + 2 * 128, M=1, ldx=ld, ldo=48) == HIP  # one row has no next
+
+
+@no_gpu
+def test_workspace_of_dispatch_on_its_own():
+    at = {n: (i + 1) * GB for i, n in enumerate(("x", "ids", "rows", "offsets", "row_slot", "slot_row", "ws"))}
+
+    def run(shape, **kw):
+        a = {n: ctypes.c_void_p(v) for n, v in {**at, **kw}.items()}
+        return ops._entry("dispatch")(a["x"], a["ids"], shape._c, a["rows"], a["offsets"], a["row_slot"],
+                                      a["slot_row"], a["ws"], GB, None)
+
+    for T in (64, 4000):  # one launch; maps that use the workspace
+        s = moe.DispatchShape(T=T, E=896, topk=16, H=512)
+        assert run(s) == HIP
+        need = moe.dispatch_query(s)
+        for n in ("x", "ids", "rows", "offsets", "row_slot", "slot_row"):
+            assert run(s, ws=at[n]) == 1, n
+            assert run(s, ws=at[n] - need + 256) == 1, n
+            assert run(s, ws=at[n] - need) == HIP, n
+    s = moe.DispatchShape(T=0, E=896, topk=16, H=512)
+    assert run(s, ws=at["offsets"]) == 1
