@@ -55,6 +55,12 @@ class _Kept:
     def __reduce__(self):
         return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
+    def _check_range(self, *names: str):
+        """ctypes cuts a number off to 32 bits, where it would name another shape."""
+        for n in names:
+            if not -2 ** 31 <= getattr(self, n) < 2 ** 31:
+                raise ValueError(f"{n} = {getattr(self, n)} is out of range")
+
 
 # A shape's C struct, torch types and array shapes are worked out at its first
 # call and kept on it: a decode step's calls are shorter than making them anew.
@@ -72,6 +78,7 @@ class DispatchShape(_Kept):
     expert_offset: int = 0
 
     def to_c(self) -> _DispatchShape:
+        self._check_range("T", "E", "topk", "H", "expert_offset")
         return _DispatchShape(self.T, self.E, self.topk, self.H, self.expert_offset,
                               DTYPE[self.dtype])
 
@@ -108,6 +115,7 @@ class W4Shape(_Kept):
     out_dtype: str = None
 
     def to_c(self, ldx: int = 0, ldo: int = 0) -> _W4Shape:
+        self._check_range("M", "N", "K", "E", "group")
         return _W4Shape(self.M, self.N, self.K, self.E, W4_FORMAT[self.format], self.group,
                         DTYPE[self.dtype], DTYPE[self.out_dtype or self.dtype], ldx, ldo)
 

@@ -80,3 +80,19 @@ def test_workspace_of_dispatch_on_its_own():
             assert run(s, ws=at[n] - need) == HIP, n
     s = moe.DispatchShape(T=0, E=896, topk=16, H=512)
     assert run(s, ws=at["offsets"]) == 1
+
+
+def test_sizes_past_32_bits_are_refused():
+    # not cut off to the C structs' 32 bits, where they would name another shape
+    big = 1 << 32
+    for kw in (dict(T=big + 4), dict(E=big + 4), dict(topk=big + 2), dict(H=big + 16), dict(expert_offset=big),
+               dict(expert_offset=-big), dict(T=1 << 31)):
+        s = moe.DispatchShape(**{**dict(T=4, E=4, topk=2, H=16), **kw})
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            s.to_c()
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            moe.dispatch_query(s)
+    for kw in (dict(M=big + 4), dict(N=big + 32), dict(K=big + 128), dict(E=big + 1), dict(group=big + 32)):
+        s = moe.W4Shape(**{**dict(M=4, N=32, K=128), **kw})
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            s.to_c()
