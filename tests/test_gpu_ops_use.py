@@ -206,3 +206,164 @@ def test_x_and_out_as_columns_of_one_matrix(odt):
             assert torch.equal(x, x0) and torch.equal(keep, keep0)
             ref, mags = f64(x) @ W[0].T, np.abs(f64(x)) @ mag[0].T
             _close(out, ref, round_tol(ref, odt, sum_tol(K) * mags), f"x first {xfirst}, grouped {grouped}")
+
+
+def test_offsets_that_count_a_row_twice_write_nowhere_else():
+    # [-7, 2, 5, -2**31, 8, 8]: experts 0, 1 own rows 0-1, 2-4, expert 3 rows 0-7; the
+    # rows that two own are one of the two results, and nothing else is written
+    E, M, N, K, G = 5, 12, 40, 256, 16
+    rng = np.random.default_rng(13)
+    m, (W, mag) = _matrices(rng, E, N, K)
+    x = torch.from_numpy(rng.standard_normal((M, K))).to(torch.bfloat16).cuda()
+    buf = torch.full((M + 2 * G, N + 5), 777.0, device="cuda")
+    out = buf[G:G + M, 2:2 + N]
+    _grouped(m, x, [-7, 2, 5, -2 ** 31, 8, 8], moe.W4Shape(M=M, N=N, K=K, E=E, out_dtype="fp32"), out=out)
+    torch.cuda.synchronize()
+    owners = [[0, 3]] * 2 + [[1, 3]] * 3 + [[3]] * 3
+    got = f64(out)
+    for r, es in enumerate(owners):
+        ok = np.zeros(N, bool)
+        for e in es:
+            ref, size = W[e] @ f64(x[r]), mag[e] @ np.abs(f64(x[r]))
+            ok |= np.abs(got[r] - ref) <= round_tol(ref, "fp32", sum_tol(K) * size)
+        assert ok.all(), r
+    buf[G:G + 8, 2:2 + N] = 777.0
+    assert bool((buf == 777.0).all())
+
+
+# ------------------------------------------------------------------ values
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_no_numbers_in_rows_that_count(dtype):
+    # NaN and infinities reach the sums they take part in, and no others
+    T, topk, E, H = 50, 3, 6, 1031
+    rng = np.random.default_rng(14)
+    ids = rng.integers(-1, E, size=(T, topk)).astype(np.int32)
+    off, row_slot, slot_row = ref_maps(ids, E, 0)
+    shape = moe.DispatchShape(T=T, E=E, topk=topk, H=H, dtype=dtype)
+    rows = torch.from_numpy(rng.standard_normal((T * topk, H))).to(TORCH[dtype]).cuda()
+    R = int(off[-1])
+    rows[2, 5], rows[7, 1030], rows[R - 1, 512], rows[R:] = float("nan"), float("inf"), -float("inf"), float("nan")
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(TORCH[dtype]).cuda()
+    dout = x.clone()
+    dout[11, 8], dout[13, 1030] = float("inf"), float("nan")
+    w = rng.standard_normal((T, topk)).astype(np.float32)
+    w[20, 1] = 0.0
+    wt, back = torch.from_numpy(w).cuda(), torch.from_numpy(slot_row.astype(np.int32)).cuda()
+
+    def same(got, ref, err, what, dt):
+        g, nan = f64(got), np.isnan(ref)
+        assert np.array_equal(np.isnan(g), nan), what
+        inf = np.isinf(ref)
+        assert np.array_equal(g[inf], ref[inf]), what
+        fin = ~(nan | inf)
+        assert (np.abs(g - ref)[fin] <= (round_tol(ref[fin], dt, err[fin]) if dt else err[fin])).all(), what
+
+    with np.errstate(invalid="ignore"):
+        ref, mag = ref_combine(f64(rows), slot_row, w.astype(np.float64))
+        same(moe.combine(rows, back, wt, shape), ref, (topk + 1) * 2.0 ** -24 * mag, "combine", dtype)
+        ref, mag = ref_combine(f64(rows), slot_row, np.ones_like(w, dtype=np.float64))
+        same(moe.dispatch_backward(rows, back, shape), ref, (topk + 1) * 2.0 ** -24 * mag, "dispatch_backward", dtype)
+        dy, dw = moe.combine_backward(dout, rows, back, wt, shape)
+        rdy, rdw, mag = ref_combine_backward(f64(dout), f64(rows), slot_row, w.astype(np.float64))
+        same(dy[:R], rdy[:R], np.abs(rdy[:R]) * 2.0 ** -24, "drows", dtype)
+        same(dw, rdw, (H / 64 + 16) * 2.0 ** -24 * mag, "dtopk_w", None)
+
+
+def test_long_ranges_of_many_experts():
+    # past 2^18 slots the maps come from ranges of 1024: 2000 experts, a last range that
+    # is ragged, ids elsewhere, a token that names an expert twice
+    T, topk, E, offset, H = 52501, 5, 2000, 48, 3
+    rng = np.random.default_rng(15)
+    ids = rng.integers(0, E + 96, size=(T, topk)).astype(np.int32)
+    ids[:, 4] = np.where(rng.random(T) < 0.2, ids[:, 0], ids[:, 4])
+    flat = ids.reshape(-1).astype(np.int64) - offset
+    here = (flat >= 0) & (flat < E)
+    order = np.argsort(np.where(here, flat, E), kind="stable")[:here.sum()]
+    slot_row = np.full(T * topk, -1, np.int64)
+    slot_row[order] = np.arange(len(order))
+    off = np.concatenate([[0], np.cumsum(np.bincount(flat[here], minlength=E))])
+    shape = moe.DispatchShape(T=T, E=E, topk=topk, H=H, expert_offset=offset)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    rows, o, rs, sr = moe.dispatch(x, torch.from_numpy(ids).cuda(), shape)
+    R = len(order)
+    assert np.array_equal(o.cpu().numpy(), off) and np.array_equal(sr.cpu().numpy().reshape(-1), slot_row)
+    assert np.array_equal(rs[:R].cpu().numpy(), order)
+    assert torch.equal(rows[:R], x[torch.from_numpy(order // topk).cuda()])
+
+
+# ------------------------------------------------------------------ tiles of 32 and 64 rows
+
+
+# M, N, K, fmt, group, dtype, zeros: many weight groups, a wave all of K or a fourth
+@pytest.mark.parametrize("case", [
+    (20, 129279, 1024, "mxfp4", 32, "bf16", False),
+    (29, 129277, 512, "int4", 64, "fp16", True),
+    (50, 129279, 1024, "mxfp4", 32, "fp16", False),
+    (61, 129270, 256, "int4", 64, "bf16", True),
+    (50, 70001, 4096, "int4", 128, "bf16", True),
+    (100, 100003, 256, "int4", 32, "fp16", True),
+], ids=lambda c: "-".join(map(str, c)))
+def test_w4_linear_of_many_rows_and_weight_groups(case):
+    M, N, K, fmt, group, dtype, zeros = case
+    say(f"[ops] linear {case}")
+    rng = np.random.default_rng(N + K)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    Np = (N + 15) // 16 * 16
+    w = torch.randint(0, 256, (Np, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    if fmt == "mxfp4":
+        sc = torch.randint(118, 128, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    else:
+        sc = (0.02 * torch.rand(N, K // group, generator=g, device="cuda")).to(TORCH[dtype])
+    z = torch.randint(0, 16, (N, K // group), generator=g, device="cuda", dtype=torch.uint8) if zeros else None
+    x = torch.from_numpy(rng.standard_normal((M, K))).to(TORCH[dtype]).cuda()
+    shape = moe.W4Shape(M=M, N=N, K=K, format=fmt, group=group, dtype=dtype, out_dtype="fp32")
+    buf = torch.full((M + 2, N + 3), 777.0, device="cuda")
+    moe.w4_linear(x, w, sc, shape, zeros=z, out=buf[1:M + 1, 1:N + 1])
+    torch.cuda.synchronize()
+    got = f64(buf)
+    buf[1:M + 1, 1:N + 1] = 777.0
+    assert bool((buf == 777.0).all())
+    # whole 16-row groups of weights: the first, some between, the last with its ragged end
+    groups = np.unique(np.concatenate([[0, Np // 16 - 2, Np // 16 - 1], rng.integers(0, Np // 16, 60)]))
+    for i in groups:
+        n1 = min(N, 16 * i + 16)
+        codes = w[16 * i:16 * i + 16].reshape(K // 128, 16, 64).transpose(0, 1).reshape(16, K // 2).cpu().numpy()
+        codes = np.stack([codes & 15, codes >> 4], -1).reshape(16, K)[:n1 - 16 * i].astype(np.int64)
+        s = sc[16 * i:n1]
+        W, mag = ref_weights(codes, s.cpu().numpy() if fmt == "mxfp4" else f64(s),
+                             None if z is None else z[16 * i:n1].cpu().numpy(), fmt, group)
+        ref, size = f64(x) @ W.T, np.abs(f64(x)) @ mag.T
+        err = np.abs(got[1:M + 1, 16 * i + 1:n1 + 1] - ref)
+        assert (err <= round_tol(ref, "fp32", sum_tol(K) * size)).all(), (i, err.max())
+
+
+# rows of each expert, rows behind, N, K, fmt, group, dtype, zeros: tiles of 64 rows
+# (more than 128 rows an expert), two weight groups a wave; K split over the waves, or
+# (the last two) not
+@pytest.mark.parametrize("case", [
+    ([200, 0, 1, 63, 64, 65, 129, 40], 700, 1040, 640, "mxfp4", 32, "bf16", False),
+    ([150, 33, 17, 0, 300, 16, 5, 130], 500, 1030, 384, "int4", 64, "fp16", True),
+    ([130, 64, 0, 7] * 16, 5100, 520, 128, "mxfp4", 32, "bf16", False),
+    ([1, 200, 33, 31] * 16, 4500, 515, 256, "int4", 64, "bf16", True),
+], ids=lambda c: "-".join(map(str, [len(c[0]), *c[1:]])))
+def test_w4_grouped_linear_of_many_rows_and_weight_groups(case):
+    counts, behind, N, K, fmt, group, dtype, zeros = case
+    say(f"[ops] grouped {case}")
+    E, R = len(counts), sum(counts)
+    M = R + behind
+    assert M // E > 128
+    rng = np.random.default_rng(N + K)
+    m, (W, mag) = _matrices(rng, E, N, K, fmt, group, dtype, zeros)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    x = torch.from_numpy(rng.standard_normal((M, K))).to(TORCH[dtype]).cuda()
+    x[R:] = float("nan")
+    out = torch.full((M, N), 777.0, device="cuda")
+    _grouped(m, x, off, moe.W4Shape(M=M, N=N, K=K, E=E, format=fmt, group=group, dtype=dtype, out_dtype="fp32"), out=out)
+    torch.cuda.synchronize()
+    assert bool((out[R:] == 777.0).all())
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        ref, size = f64(x[lo:hi]) @ W[e].T, np.abs(f64(x[lo:hi])) @ mag[e].T
+        _close(out[lo:hi], ref, round_tol(ref, "fp32", sum_tol(K) * size), f"expert {e}")
