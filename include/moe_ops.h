@@ -155,7 +155,10 @@ int moe_ops_combine_backward(const void* dout_dev, const void* rows_dev,
  * sum in 32 bits. With bfloat16 tokens MXFP4 scales are applied to the codes,
  * which is exact too: scale bytes up to 252 (then no weight passes the
  * type's range; bytes 253 and 254 may give infinities). INT4 zero points come
- * off a group's sum, so an infinite x gives NaN there.
+ * off a group's sum: the 32-bit rounding goes by the sum of |s| (c + z) |x|, not
+ * |s| |c - z| |x|, so weights that equal their zero points need not give exactly
+ * 0, and NaN comes out where x is infinite or s times the sum of c x or of z x
+ * passes the 32-bit range.
  *
  * Deterministic. For one shape a row's result depends, to the bit, on the row and
  * its matrix alone: not on its place in x, nor on the other rows and their experts.

@@ -37,7 +37,7 @@ typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 // 16-byte buffer load of weights, non-temporal (cache-policy operand 2) where
 // they are read once: 64-token decode of 896 experts 143 us against 164 with
 // plain loads. Where several row tiles read them (64 experts of 32 rows) plain
-// loads take 127 us, these 135; a branch around the two kinds of load costs the
+// loads take 121 us, these 131; a branch around the two kinds of load costs the
 // first case 6 % (its waits then cover both), so the walk is an instance of each.
 template <bool ONCE>
 __device__ __forceinline__ uint4 bld16_once(__amdgpu_buffer_rsrc_t r, uint32_t off) {
@@ -613,17 +613,17 @@ void w4_go(const W4Args& a0, int64_t U, hipStream_t st) {
 //   LDS. It is chosen where its estimate is not the higher one:
 //   16-row tiles (the weights' stream bounds them): rounds of resident blocks (three a
 //   CU) times (steps + 4), the 4 for a task's start and end. K 384 x N 3584 of 896
-//   experts: 98 us against 204 with kw = 4; K 7168 x N 4096 of 64 experts: 166 against
-//   135. Up to 30 KB of scales a block leave room for three with kw = 1 too; from there
+//   experts: 97 us against 205 with kw = 4; K 7168 x N 4096 of 64 experts: 176 against
+//   157. Up to 30 KB of scales a block leave room for three with kw = 1 too; from there
 //   to the limit of 36 two fit, which costs MXFP4 little (K 4096: N 2816 of 60 experts
 //   137 against 138, N 768 of 448 138 against 128) and INT4 nothing (groups of 64 with
 //   zero points, K 2560: N 768 of 896 experts 173 against 197).
 //   32 and 64 rows (decode, MFMAs and LDS bound them, so what the busiest CU has to do
 //   counts): tasks a CU times (steps + 2.5 or 2), and where a CU has one block at a
-//   time, which leaves its waits open, a third more with MXFP4, two with INT4. N 129279, 64 rows: K 1024 47 us with kw = 1, 71 with 4; INT4 of 64
-//   with zero points at K 2048 148 and 125, at K 4096 258 and 203, since kw = 1 leaves
-//   room for one block; N 65536, K 4096, 32 rows 46 and 51; 16 experts of 256 rows,
-//   K 3584, N 4096 362 and 312.
+//   time, which leaves its waits open, a third more with MXFP4, two with INT4. N 129279, 64 rows: K 1024 48 us with kw = 1, 72 with 4; INT4 of 64
+//   with zero points at K 2048 149 and 126, at K 4096 262 and 204, since kw = 1 leaves
+//   room for one block; N 65536, K 4096, 32 rows 47 and 51; 16 experts of 256 rows,
+//   K 3584, N 4096 352 and 312.
 // - Fewer: RB = 2, or 1 up to a group a CU, and K over eight waves from 16 steps on.
 //   8192 x 8192, 1 and 16 tokens: 9.3 and 12.3 us with RB = 2 and eight waves, 9.7
 //   and 15.3 with RB = 1, 13.4 and 15.6 with RB = 4 and four waves. 4096 x 4096:
@@ -631,13 +631,13 @@ void w4_go(const W4Args& a0, int64_t U, hipStream_t st) {
 //   and four waves, 8.8 with RB = 4.
 // Row tiles of x a task takes (MT): 16 rows, whose tiles read their weights again
 // from the caches, or 32 (up to 32 rows of one matrix) or 64, which share a decode.
-// N 32768, K 4096, MXFP4, 32 and 64 rows: 28 and 42 us so, 31 and 58 in tiles of
-// 16; INT4 of 64 33 and 54, 35 and 66. INT4 of 32 runs out of registers with 64
+// N 32768, K 4096, MXFP4, 32 and 64 rows: 26 and 42 us so, 27 and 45 in tiles of
+// 16; INT4 of 64 32 and 55, 31 and 55. INT4 of 32 runs out of registers with 64
 // rows (82 us against 75). The rows of an expert are not known here, only M / E,
 // which counts those that live elsewhere too, so experts take tiles of 16 until
 // M / E says many: K 2048 x N 4096, a quarter of 256 experts, M / E = 64 with 16
-// rows each, 84 us in tiles of 16, 133 in tiles of 64; M / E = 1024 with 256 rows
-// each (K 3584, N 768, 16 experts) 113 and 69.
+// rows each, 77 us in tiles of 16, 122 in tiles of 64; 16 experts of 256 rows
+// (K 3584, N 768) 85 and 71.
 template <int FMT, int G, int DT>
 void w4_rows(const W4Args& a, hipStream_t st) {
   constexpr bool kWide = !(FMT == MOE_W4_INT4 && G == 32);
