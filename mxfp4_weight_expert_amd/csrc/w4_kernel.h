@@ -620,10 +620,11 @@ void w4_go(const W4Args& a0, int64_t U, hipStream_t st) {
 //   zero points, K 2560: N 768 of 896 experts 173 against 197).
 //   32 and 64 rows (decode, MFMAs and LDS bound them, so what the busiest CU has to do
 //   counts): tasks a CU times (steps + 2.5 or 2), and where a CU has one block at a
-//   time, which leaves its waits open, a third more with MXFP4, two with INT4. N 129279, 64 rows: K 1024 48 us with kw = 1, 72 with 4; INT4 of 64
-//   with zero points at K 2048 149 and 126, at K 4096 262 and 204, since kw = 1 leaves
-//   room for one block; N 65536, K 4096, 32 rows 47 and 51; 16 experts of 256 rows,
-//   K 3584, N 4096 352 and 312.
+//   time, which leaves its waits open, a third more with MXFP4, two with INT4.
+//   N 129279, 64 rows: K 1024 48 us with kw = 1, 72 with 4; INT4 of 64 with zero
+//   points at K 2048 149 and 126, at K 4096 262 and 204, since kw = 1 leaves room for
+//   one block; N 65536, K 4096, 32 rows 47 and 51; 16 experts of 256 rows, K 3584,
+//   N 4096 352 and 312.
 // - Fewer: RB = 2, or 1 up to a group a CU, and K over eight waves from 16 steps on.
 //   8192 x 8192, 1 and 16 tokens: 9.3 and 12.3 us with RB = 2 and eight waves, 9.7
 //   and 15.3 with RB = 1, 13.4 and 15.6 with RB = 4 and four waves. 4096 x 4096:
