@@ -55,11 +55,13 @@ class _Kept:
     def __reduce__(self):
         return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
-    def _check_range(self, *names: str):
+    @functools.cached_property
+    def _fits(self) -> bool:
         """ctypes cuts a number off to 32 bits, where it would name another shape."""
-        for n in names:
+        for n in self._sizes:
             if not -2 ** 31 <= getattr(self, n) < 2 ** 31:
                 raise ValueError(f"{n} = {getattr(self, n)} is out of range")
+        return True
 
 
 # A shape's C struct, torch types and array shapes are worked out at its first
@@ -76,9 +78,10 @@ class DispatchShape(_Kept):
     H: int
     dtype: str = "bf16"
     expert_offset: int = 0
+    _sizes = ("T", "E", "topk", "H", "expert_offset")
 
     def to_c(self) -> _DispatchShape:
-        self._check_range("T", "E", "topk", "H", "expert_offset")
+        self._fits
         return _DispatchShape(self.T, self.E, self.topk, self.H, self.expert_offset,
                               DTYPE[self.dtype])
 
@@ -113,9 +116,10 @@ class W4Shape(_Kept):
     group: int = 32
     dtype: str = "bf16"
     out_dtype: str = None
+    _sizes = ("M", "N", "K", "E", "group")
 
     def to_c(self, ldx: int = 0, ldo: int = 0) -> _W4Shape:
-        self._check_range("M", "N", "K", "E", "group")
+        self._fits
         return _W4Shape(self.M, self.N, self.K, self.E, W4_FORMAT[self.format], self.group,
                         DTYPE[self.dtype], DTYPE[self.out_dtype or self.dtype], ldx, ldo)
 
