@@ -3,8 +3,8 @@
 Argument marshalling only: every step of the layer runs in the library's HIP
 kernels. PyTorch supplies device memory and the current stream. The names
 mirror the C ABI in include/moe_mxfp4.h: query, workspace_layout, forward,
-strerror; the operators of include/moe_ops.h (dispatch, combine, 4-bit products) are in ops.py and
-exported here. There is no fallback: without the built library every call raises.
+strerror; the operators of include/moe_ops.h (dispatch, combine, 4-bit products) are in ops.py, those
+of include/moe_linear.h (16-bit products with their gradients, adapters) in linear.py, all exported here. There is no fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
@@ -15,7 +15,8 @@ from dataclasses import dataclass
 __all__ = ["Shape", "query", "workspace_layout", "forward", "forward_timed", "forward_noalloc",
            "strerror", "lib_path", "MoeError", "read_maps", "ADTYPE", "GEMM2_PATH", "load_library",
            "prepack", "DispatchShape", "W4Shape", "dispatch_query", "dispatch", "dispatch_backward",
-           "combine", "combine_backward", "w4_linear", "w4_grouped_linear"]
+           "combine", "combine_backward", "w4_linear", "w4_grouped_linear", "LinearShape", "GatedShape",
+           "grouped_linear", "grouped_linear_backward", "gated_linear", "gated_linear_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoe_mxfp4.so")
@@ -293,3 +294,5 @@ def read_maps(workspace, shape: Shape) -> dict:
 
 from .ops import (DispatchShape, W4Shape, combine, combine_backward, dispatch,  # noqa: E402
                   dispatch_backward, dispatch_query, w4_grouped_linear, w4_linear)
+from .linear import (GatedShape, LinearShape, gated_linear, gated_linear_backward,  # noqa: E402
+                     grouped_linear, grouped_linear_backward)

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "common.h"
+
 namespace moe {
 
 struct RouteArgs {
@@ -147,6 +149,39 @@ struct W4Args {
 };
 hipError_t launch_w4(const W4Args& a, hipStream_t st);
 hipError_t launch_w4_bf16(const W4Args& a, hipStream_t st);  // launch_w4's
+
+// Tiles a 16-bit product may have.
+constexpr int64_t kMaxTileItems = int64_t{1} << 30;
+// out[c, r] = sum over i of P[r, i] Q[c, i] (tile_product.h).
+struct TileArgs {
+  const void* p;
+  const void* q;
+  void* out;               // rows ldo apart
+  void* gu;                // gated forward: [M, 2 R] pre-activations, or null
+  const int32_t* offsets;  // [E + 1] or null
+  int M, E;                // rows of all experts; matrices
+  int R;                   // r: elements of a row of out (gated: features)
+  int C;                   // gradient of the matrices: rows of one
+  int I;                   // i to sum over, where it is not the expert's rows
+  int64_t pstride;         // elements from one matrix of P to the next
+  int64_t ldp, ldq, ldo;   // elements from row to row
+  int dtype, out_dtype;
+  ActArgs act;             // gated
+};
+hipError_t launch_tile_forward(const TileArgs& a, bool gated, hipStream_t st);
+hipError_t launch_tile_row_grad(const TileArgs& a, hipStream_t st);
+hipError_t launch_tile_mat_grad(const TileArgs& a, hipStream_t st);
+
+// Gradient of the activation: dgu [M, 2 I] from dh [M, I] and the pre-activations.
+struct ActGradArgs {
+  const void* dh;
+  const void* gu;
+  void* dgu;
+  const int32_t* offsets;  // or null
+  int M, I, E, dtype;
+  ActArgs act;
+};
+hipError_t launch_act_grad(const ActGradArgs& a, hipStream_t st);
 
 hipError_t launch_prepack(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t row_bytes,
                           hipStream_t st);

@@ -1,0 +1,241 @@
+// C ABI of the 16-bit products (moe_linear.h): argument checks, then the launches.
+#include "checks.h"
+#include "common.h"
+#include "kernels.h"
+#include "moe_linear.h"
+
+#include <cmath>
+
+using namespace moe;
+
+namespace {
+
+// Elements of a row or from row to row, and of a matrix: byte offsets inside a tile
+// (256 rows) and inside a matrix stay below the 2^31 that buffer accesses of the
+// kernels count to.
+constexpr int64_t kMaxLd = int64_t{1} << 20;
+constexpr int64_t kMaxMatrix = int64_t{1} << 30;
+
+bool half_type(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16; }
+
+// A product of M rows of K elements with E matrices of N rows.
+struct Product {
+  int64_t M, N, K, E, ldx, ldo, out_cols;  // out_cols: elements of a row of the result
+  int dtype, out_dtype;
+};
+
+int check(const Product& p) {
+  if (p.M < 0 || p.N < 1 || p.K < 1 || p.E < 1) return MOE_ERR_INVALID;
+  if (p.N % 8 != 0 || p.K % 8 != 0 || p.ldx % 8 != 0 || p.ldo % 8 != 0 || p.out_cols % 8 != 0) return MOE_ERR_INVALID;
+  if ((p.ldx != 0 && p.ldx < p.K) || (p.ldo != 0 && p.ldo < p.out_cols)) return MOE_ERR_INVALID;
+  if (p.M > kMaxSlots || p.N > kMaxLd || p.K > kMaxLd || p.ldx > kMaxLd || p.ldo > kMaxLd || p.E > kMaxExperts ||
+      p.N * p.K > kMaxMatrix || !half_type(p.dtype) || (p.out_dtype != p.dtype && p.out_dtype != MOE_DTYPE_FP32))
+    return MOE_ERR_UNSUPPORTED;
+  if ((p.M / 16 + p.E + 1) * (p.N / 16 + 1) >= kMaxTileItems) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int check(const moe_linear_shape* s, Product& p) {
+  if (s == nullptr) return MOE_ERR_INVALID;
+  p = {s->M, s->N, s->K, s->E, s->ldx, s->ldo, s->N, s->dtype, s->out_dtype};
+  return check(p);
+}
+
+int check(const moe_gated_shape* s, Product& p) {
+  if (s == nullptr || s->I < 1) return MOE_ERR_INVALID;
+  p = {s->M, int64_t{2} * s->I, s->H, s->E, s->ldx, s->ldo, s->I, s->dtype, s->dtype};
+  const bool situ = s->activation == MOE_ACT_SITU;
+  if (!std::isfinite(s->swiglu_limit)) return MOE_ERR_INVALID;
+  if (situ && !(std::isfinite(s->act_beta) && s->act_beta > 0.0f && std::isfinite(s->act_linear_beta) &&
+                s->act_linear_beta > 0.0f))
+    return MOE_ERR_INVALID;
+  const int rc = check(p);
+  if (rc != MOE_OK) return rc;
+  return situ || s->activation == MOE_ACT_SWIGLU ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+ActArgs act_args(const moe_gated_shape& s) {
+  const bool situ = s.activation == MOE_ACT_SITU;
+  ActArgs a{};
+  a.kind = s.activation;
+  a.limit = s.swiglu_limit;
+  a.beta = s.act_beta;
+  a.inv_beta = situ ? 1.0f / s.act_beta : 0.0f;
+  a.lb = s.act_linear_beta;
+  a.inv_lb = situ ? 1.0f / s.act_linear_beta : 0.0f;
+  return a;
+}
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+// Whether an output meets an input or another output.
+template <int NO, int NI>
+bool meet(const Range (&out)[NO], const Range (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i].p, out[i].bytes, r.p, r.bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+  }
+  return false;
+}
+
+int64_t offsets_bytes(const Product& p) { return (p.E + 1) * 4; }
+
+TileArgs tile_args(const Product& p, const int32_t* offsets) {
+  TileArgs a{};
+  a.offsets = offsets;
+  a.M = static_cast<int>(p.M);
+  a.E = static_cast<int>(p.E);
+  a.pstride = p.N * p.K;
+  a.dtype = p.dtype;
+  a.out_dtype = p.dtype;
+  return a;
+}
+
+int forward(const Product& p, const void* x, const int32_t* offsets, const void* w, void* out, void* gu,
+            const ActArgs* act, void* stream) {
+  if (offsets == nullptr && p.E != 1) return MOE_ERR_INVALID;
+  if (p.M == 0) return MOE_OK;
+  if (x == nullptr || w == nullptr || out == nullptr) return MOE_ERR_INVALID;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(gu, 16) || !aligned(offsets, 4))
+    return MOE_ERR_INVALID;
+  const int64_t ldx = p.ldx != 0 ? p.ldx : p.K, ldo = p.ldo != 0 ? p.ldo : p.out_cols, so = size_of(p.out_dtype);
+  const Range outs[2] = {{out, ((p.M - 1) * ldo + p.out_cols) * so}, {gu, p.M * p.N * 2}};
+  const Range ins[2] = {{w, p.E * p.N * p.K * 2}, {offsets, offsets_bytes(p)}};
+  if (meet(outs, ins) || overlap(gu, outs[1].bytes, x, ((p.M - 1) * ldx + p.K) * 2) ||
+      rows_overlap(x, p.K * 2, ldx * 2, out, p.out_cols * so, ldo * so, p.M))
+    return MOE_ERR_INVALID;
+  TileArgs a = tile_args(p, offsets);
+  a.p = w;
+  a.q = x;
+  a.out = out;
+  a.gu = gu;
+  a.R = static_cast<int>(p.out_cols);
+  a.I = static_cast<int>(p.K);
+  a.ldp = p.K;
+  a.ldq = ldx;
+  a.ldo = ldo;
+  a.out_dtype = p.out_dtype;
+  if (act != nullptr) a.act = *act;
+  return status(launch_tile_forward(a, act != nullptr, static_cast<hipStream_t>(stream)));
+}
+
+// What both backward passes ask of their shape.
+int check_backward(const Product& p, const int32_t* offsets) {
+  if (p.ldx != 0 || p.ldo != 0 || (offsets == nullptr && p.E != 1)) return MOE_ERR_INVALID;
+  if (p.E * (p.N / 256 + 1) * (p.K / 256 + 1) >= kMaxTileItems) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// dx and dw from the gradient of the product, either of them null.
+int gradients(const Product& p, const void* dout, const void* x, const int32_t* offsets, const void* w, void* dx,
+              void* dw, hipStream_t st) {
+  if (dx != nullptr && p.M > 0) {
+    TileArgs a = tile_args(p, offsets);
+    a.p = w;
+    a.q = dout;
+    a.out = dx;
+    a.R = static_cast<int>(p.K);
+    a.I = static_cast<int>(p.N);
+    a.ldp = a.ldo = p.K;
+    a.ldq = p.N;
+    const int rc = status(launch_tile_row_grad(a, st));
+    if (rc != MOE_OK) return rc;
+  }
+  if (dw != nullptr) {
+    TileArgs a = tile_args(p, offsets);
+    a.p = x;
+    a.q = dout;
+    a.out = dw;
+    a.R = static_cast<int>(p.K);
+    a.C = static_cast<int>(p.N);
+    a.ldp = a.ldo = p.K;
+    a.ldq = p.N;
+    a.out_dtype = p.out_dtype;
+    return status(launch_tile_mat_grad(a, st));
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_linear_grouped(const void* x_dev, const int32_t* offsets_dev, const void* w_dev,
+                       const moe_linear_shape* shape, void* out_dev, void* stream) {
+  Product p;
+  const int rc = check(shape, p);
+  return rc != MOE_OK ? rc : forward(p, x_dev, offsets_dev, w_dev, out_dev, nullptr, nullptr, stream);
+}
+
+int moe_linear_grouped_backward(const void* dout_dev, const void* x_dev, const int32_t* offsets_dev,
+                                const void* w_dev, const moe_linear_shape* shape, void* dx_dev,
+                                void* dw_dev, void* stream) {
+  Product p;
+  int rc = check(shape, p);
+  if (rc == MOE_OK) rc = check_backward(p, offsets_dev);
+  if (rc != MOE_OK) return rc;
+  if (p.M > 0 && ((dx_dev != nullptr && w_dev == nullptr) || (dw_dev != nullptr && x_dev == nullptr) ||
+                  ((dx_dev != nullptr || dw_dev != nullptr) && dout_dev == nullptr)))
+    return MOE_ERR_INVALID;
+  if (!aligned(dout_dev, 16) || !aligned(x_dev, 16) || !aligned(w_dev, 16) || !aligned(dx_dev, 16) ||
+      !aligned(dw_dev, 16) || !aligned(offsets_dev, 4))
+    return MOE_ERR_INVALID;
+  const int64_t matrices = p.E * p.N * p.K;
+  const Range outs[2] = {{dx_dev, p.M * p.K * 2}, {dw_dev, matrices * size_of(p.out_dtype)}};
+  const Range ins[4] = {{dout_dev, p.M * p.N * 2},
+                        {x_dev, dw_dev != nullptr ? p.M * p.K * 2 : 0},
+                        {w_dev, dx_dev != nullptr ? matrices * 2 : 0},
+                        {offsets_dev, offsets_bytes(p)}};
+  if (meet(outs, ins)) return MOE_ERR_INVALID;
+  return gradients(p, dout_dev, x_dev, offsets_dev, w_dev, dx_dev, dw_dev, static_cast<hipStream_t>(stream));
+}
+
+int moe_linear_gated(const void* x_dev, const int32_t* offsets_dev, const void* w13_dev,
+                     const moe_gated_shape* shape, void* h_dev, void* gu_dev, void* stream) {
+  Product p;
+  const int rc = check(shape, p);
+  if (rc != MOE_OK) return rc;
+  const ActArgs act = act_args(*shape);
+  return forward(p, x_dev, offsets_dev, w13_dev, h_dev, gu_dev, &act, stream);
+}
+
+int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32_t* offsets_dev,
+                              const void* gu_dev, const void* w13_dev, const moe_gated_shape* shape,
+                              void* dgu_dev, void* dx_dev, void* dw_dev, void* stream) {
+  Product p;
+  int rc = check(shape, p);
+  if (rc == MOE_OK) rc = check_backward(p, offsets_dev);
+  if (rc != MOE_OK) return rc;
+  if (p.M > 0 && (dh_dev == nullptr || gu_dev == nullptr || dgu_dev == nullptr ||
+                  (dx_dev != nullptr && w13_dev == nullptr) || (dw_dev != nullptr && x_dev == nullptr)))
+    return MOE_ERR_INVALID;
+  if (!aligned(dh_dev, 16) || !aligned(x_dev, 16) || !aligned(gu_dev, 16) || !aligned(w13_dev, 16) ||
+      !aligned(dgu_dev, 16) || !aligned(dx_dev, 16) || !aligned(dw_dev, 16) || !aligned(offsets_dev, 4))
+    return MOE_ERR_INVALID;
+  const int64_t matrices = p.E * p.N * p.K * 2, pre = p.M * p.N * 2, rows = p.M * p.K * 2;
+  const Range outs[3] = {{dgu_dev, pre}, {dx_dev, rows}, {dw_dev, matrices}};
+  const Range ins[5] = {{dh_dev, pre / 2}, {gu_dev, pre}, {x_dev, dw_dev != nullptr ? rows : 0},
+                        {w13_dev, dx_dev != nullptr ? matrices : 0}, {offsets_dev, offsets_bytes(p)}};
+  if (meet(outs, ins)) return MOE_ERR_INVALID;
+  if (p.M > 0) {
+    ActGradArgs g{};
+    g.dh = dh_dev;
+    g.gu = gu_dev;
+    g.dgu = dgu_dev;
+    g.offsets = offsets_dev;
+    g.M = shape->M;
+    g.I = shape->I;
+    g.E = shape->E;
+    g.dtype = shape->dtype;
+    g.act = act_args(*shape);
+    rc = status(launch_act_grad(g, static_cast<hipStream_t>(stream)));
+    if (rc != MOE_OK) return rc;
+  }
+  return gradients(p, dgu_dev, x_dev, offsets_dev, w13_dev, dx_dev, dw_dev, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,5 +1,6 @@
 // C ABI of the dispatch, combine and 4-bit product operators (moe_ops.h):
 // argument checks, then the launches.
+#include "checks.h"
 #include "common.h"
 #include "kernels.h"
 #include "moe_ops.h"
@@ -8,34 +9,10 @@ using namespace moe;
 
 namespace {
 
-constexpr int64_t kMaxSlots = int64_t{1} << 23;
 constexpr int64_t kMaxRowLen = int64_t{1} << 24;  // H, N, ldx, ldo
 // T * H: keeps the grids (a one-wave block for 1 KB of a token) within the 2^32
 // threads of a launch
 constexpr int64_t kMaxElems = int64_t{1} << 33;
-
-bool known_dtype(int d) {
-  return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_FP16 || d == MOE_DTYPE_FP32;
-}
-int64_t size_of(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) &&
-         y < x + static_cast<uintptr_t>(na);
-}
-
-// Rows of two matrices, `rows` of each, na and nb bytes long and sa and sb apart. With
-// the same stride the rows of the one may lie between those of the other; with
-// different ones the ranges decide.
-bool rows_overlap(const void* a, int64_t na, int64_t sa, const void* b, int64_t nb, int64_t sb,
-                  int64_t rows) {
-  if (!overlap(a, (rows - 1) * sa + na, b, (rows - 1) * sb + nb)) return false;
-  if (sa != sb) return true;
-  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
-  const int64_t at = (d % sa + sa) % sa;  // from a row of a to the next row of b
-  return at < na || at + nb > sa;
-}
 
 int check(const moe_ops_dispatch_shape* s) {
   if (s == nullptr) return MOE_ERR_INVALID;
@@ -60,8 +37,6 @@ DispatchWs dispatch_ws(const moe_ops_dispatch_shape& s) {
   const uint64_t counts = (ranges * s.E * 4 + 255) / 256 * 256;
   return {counts, counts + (static_cast<uint64_t>(s.E) * 4 + 255) / 256 * 256};
 }
-
-int status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // Bytes of the token and slot arrays of a shape.
 struct Extents {

@@ -207,19 +207,23 @@ def _on_stream(stream: int, t):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device))
 
 
-def _run(name: str, index: int, *args):
+def _call(entry, name: str, index: int, args):
     """Call an entry point on the GPU's current stream, with that GPU current (the
     library launches there)."""
     if index < 0:
         raise ValueError("tensors must be on the GPU")
     stream = torch._C._cuda_getCurrentRawStream(index)
     if index == torch._C._cuda_getDevice():
-        rc = _entry(name)(*args, stream)
+        rc = entry(*args, stream)
     else:
         with torch.cuda.device(index):
-            rc = _entry(name)(*args, stream)
+            rc = entry(*args, stream)
     if rc != MOE_OK:
-        raise MoeError(rc, "moe_ops_" + name)
+        raise MoeError(rc, name)
+
+
+def _run(name: str, index: int, *args):
+    _call(_entry(name), "moe_ops_" + name, index, args)
 
 
 def dispatch_query(shape: DispatchShape) -> int:
