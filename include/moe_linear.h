@@ -135,6 +135,74 @@ int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32
                               const void* gu_dev, const void* w13_dev, const moe_gated_shape* shape,
                               void* dgu_dev, void* dx_dev, void* dw_dev, void* stream);
 
+/*
+ * Shape of the adapters' product out[m, n] = base[m, n] + scale[i] * sum over r
+ * of t[m, r] b[i, n, r], t[m, r] = sum over k of x[m, k] a[i, r, k], i the
+ * adapter of row m; a row without one gets base[m, n].
+ *
+ *   M             rows (0 allowed), up to 2^23
+ *   N             elements of a row of out, 1..2^20: any length
+ *   K             elements of a row of x, a multiple of 8 up to 2^20
+ *   R             rank: a multiple of 8, 8..128 (adapters of lower rank end in
+ *                 zeros)
+ *   A             adapters, 1..2048
+ *   dtype         MOE_DTYPE_BF16 or MOE_DTYPE_FP16: x, a and b
+ *   out_dtype     dtype or MOE_DTYPE_FP32: base and out
+ *   ldx, ldb, ldo elements from one row of x / base / out to the next; 0 stands
+ *                 for K / N / N; ldx a multiple of 8; each up to 2^20
+ *
+ * t is held in 32 bits and enters the second product as two values of dtype
+ * whose sum is t to 2^-16 of it or better (of the row's largest |t| in fp16).
+ */
+typedef struct moe_adapter_shape {
+  int32_t M;
+  int32_t N;
+  int32_t K;
+  int32_t R;
+  int32_t A;
+  int32_t dtype;
+  int32_t out_dtype;
+  int64_t ldx;
+  int64_t ldb;
+  int64_t ldo;
+} moe_adapter_shape;
+
+/*
+ * Check a shape and return the workspace bytes of both calls below (at least
+ * 256). Host only. MOE_ERR_INVALID: null pointer, sizes below their range, K, R
+ * or ldx no multiple of 8, strides shorter than a row; MOE_ERR_UNSUPPORTED:
+ * sizes above theirs, unknown type.
+ */
+int moe_linear_adapter_query(const moe_adapter_shape* shape, uint64_t* workspace_bytes);
+
+/*
+ * Maps that sort the rows by adapter, for all calls with the same ids. ids_dev
+ * int32 [M]: a row's adapter, any value outside [0, A) for none. offsets_dev
+ * int32 [A + 1], row_slot_dev and slot_row_dev int32 [M]: as moe_ops_dispatch
+ * writes them for one column, row_slot's entries from offsets[A] on left as
+ * they were. Errors as moe_ops_dispatch.
+ */
+int moe_linear_adapter_maps(const int32_t* ids_dev, const moe_adapter_shape* shape,
+                            int32_t* offsets_dev, int32_t* row_slot_dev, int32_t* slot_row_dev,
+                            void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
+/*
+ * x_dev [M, K] and a_dev [A, R, K], b_dev [A, N, R] 16-byte aligned; scale_dev
+ * float [A], or NULL: 1; base_dev [M, N], or NULL: 0; out_dev [M, N], which may
+ * be base_dev with the same stride (rows without an adapter are then not
+ * touched). Entries of row_slot outside [0, M) are left out. Alignment: base
+ * and out their element size, maps and scale 4 bytes, workspace 256 bytes.
+ *
+ * MOE_ERR_WORKSPACE: workspace NULL, too small or misaligned; MOE_ERR_INVALID:
+ * null or misaligned pointers, out overlapping an input (base apart, as above)
+ * or the workspace anything. Calls that may overlap in time need workspaces of
+ * their own.
+ */
+int moe_linear_adapter(const void* x_dev, const int32_t* offsets_dev, const int32_t* row_slot_dev,
+                       const int32_t* slot_row_dev, const void* a_dev, const void* b_dev,
+                       const float* scale_dev, const moe_adapter_shape* shape, const void* base_dev,
+                       void* out_dev, void* workspace_dev, uint64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,8 @@ __all__ = ["Shape", "query", "workspace_layout", "forward", "forward_timed", "fo
            "strerror", "lib_path", "MoeError", "read_maps", "ADTYPE", "GEMM2_PATH", "load_library",
            "prepack", "DispatchShape", "W4Shape", "dispatch_query", "dispatch", "dispatch_backward",
            "combine", "combine_backward", "w4_linear", "w4_grouped_linear", "LinearShape", "GatedShape",
-           "grouped_linear", "grouped_linear_backward", "gated_linear", "gated_linear_backward"]
+           "grouped_linear", "grouped_linear_backward", "gated_linear", "gated_linear_backward",
+           "AdapterShape", "adapter_query", "adapter_maps", "adapter_linear"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoe_mxfp4.so")
@@ -294,5 +295,6 @@ def read_maps(workspace, shape: Shape) -> dict:
 
 from .ops import (DispatchShape, W4Shape, combine, combine_backward, dispatch,  # noqa: E402
                   dispatch_backward, dispatch_query, w4_grouped_linear, w4_linear)
-from .linear import (GatedShape, LinearShape, gated_linear, gated_linear_backward,  # noqa: E402
-                     grouped_linear, grouped_linear_backward)
+from .linear import (AdapterShape, GatedShape, LinearShape, adapter_linear, adapter_maps,  # noqa: E402
+                     adapter_query, gated_linear, gated_linear_backward, grouped_linear,
+                     grouped_linear_backward)

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kernels.h"
 #include "moe_ops.h"
 
 namespace moe {
@@ -31,6 +32,18 @@ inline bool rows_overlap(const void* a, int64_t na, int64_t sa, const void* b, i
   const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
   const int64_t at = (d % sa + sa) % sa;  // from a row of a to the next row of b
   return at < na || at + nb > sa;
+}
+
+// Workspace of the maps of `slots` slots: range counts at 0, then the experts' counts.
+struct MapsWs {
+  uint64_t counts, bytes;
+};
+inline MapsWs maps_ws(uint64_t slots, uint64_t E) {
+  if (slots <= static_cast<uint64_t>(kFusedSlots)) return {0, 256};
+  const uint64_t len = map_range_slots(static_cast<int64_t>(slots));
+  const uint64_t ranges = (slots + len - 1) / len;
+  const uint64_t counts = (ranges * E * 4 + 255) / 256 * 256;
+  return {counts, counts + (E * 4 + 255) / 256 * 256};
 }
 
 inline int status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }

@@ -152,7 +152,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
   m.row_slot = a.row_slot;
   m.slot_row = a.slot_row;
   const hipError_t err = launch_sort_maps(m, st);
-  if (err != hipSuccess) return err;
+  if (err != hipSuccess || row_bytes == 0) return err;  // no rows: the maps alone
   const int npiece = static_cast<int>((row_bytes + 1023) / 1024);
   hipLaunchKernelGGL(dispatch_copy_kernel, dim3(static_cast<unsigned>(a.T) * npiece), dim3(64), 0,
                      st, a.x, a.slot_row, a.topk, row_bytes, npiece, a.rows);

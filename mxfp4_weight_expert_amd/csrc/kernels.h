@@ -105,7 +105,8 @@ struct SortMapsArgs {
 int map_range_slots(int64_t nslots);
 hipError_t launch_sort_maps(const SortMapsArgs& a, hipStream_t st);
 
-// Slots up to which dispatch is one launch (dispatch.hip).
+// Slots up to which dispatch is one launch (dispatch.hip). H = 0: the maps alone, x
+// and rows are not touched.
 constexpr int kFusedSlots = 4096;
 struct DispatchArgs {
   const uint8_t* x;    // [T, H]
@@ -182,6 +183,26 @@ struct ActGradArgs {
   ActArgs act;
 };
 hipError_t launch_act_grad(const ActGradArgs& a, hipStream_t st);
+
+// Low-rank adapters (adapter.hip): out = base + scale[a] (x A_a^T) B_a^T for the rows
+// that the maps sort by adapter.
+struct AdapterArgs {
+  const void* x;             // [M, K], rows ldx apart
+  const int32_t* offsets;    // [A + 1]
+  const int32_t* row_slot;   // sorted row -> row
+  const int32_t* slot_row;   // row -> sorted row, or -1
+  const void* a;             // [A, R, K]
+  const void* b;             // [A, N, R]
+  const float* scale;        // [A] or null: 1
+  const void* base;          // [M, N], rows ldb apart, or null
+  void* out;                 // [M, N], rows ldo apart; may be base
+  float* part;               // workspace: [splits, M, R], x A^T by part of K
+  int M, N, K, R, A, splits, dtype, out_dtype;
+  int64_t ldx, ldb, ldo;
+};
+// Parts of K that the first product is split into.
+int adapter_splits(int64_t M, int64_t A, int64_t K);
+hipError_t launch_adapter(const AdapterArgs& a, hipStream_t st);
 
 hipError_t launch_prepack(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t row_bytes,
                           hipStream_t st);

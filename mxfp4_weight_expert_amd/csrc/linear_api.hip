@@ -160,9 +160,125 @@ int gradients(const Product& p, const void* dout, const void* x, const int32_t* 
   return MOE_OK;
 }
 
+int check(const moe_adapter_shape* s) {
+  if (s == nullptr) return MOE_ERR_INVALID;
+  if (s->M < 0 || s->N < 1 || s->K < 1 || s->R < 1 || s->A < 1) return MOE_ERR_INVALID;
+  if (s->K % 8 != 0 || s->R % 8 != 0 || s->ldx % 8 != 0) return MOE_ERR_INVALID;
+  if ((s->ldx != 0 && s->ldx < s->K) || (s->ldb != 0 && s->ldb < s->N) || (s->ldo != 0 && s->ldo < s->N))
+    return MOE_ERR_INVALID;
+  if (s->M > kMaxSlots || s->N > kMaxLd || s->K > kMaxLd || s->R > 128 || s->A > kMaxExperts || s->ldx > kMaxLd ||
+      s->ldb > kMaxLd || s->ldo > kMaxLd || !half_type(s->dtype) ||
+      (s->out_dtype != s->dtype && s->out_dtype != MOE_DTYPE_FP32))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// t by part of K; the maps' workspace where it is larger.
+uint64_t adapter_ws(const moe_adapter_shape& s) {
+  const uint64_t part = static_cast<uint64_t>(adapter_splits(s.M, s.A, s.K)) * s.M * s.R * 4;
+  const uint64_t both = part > maps_ws(s.M, s.A).bytes ? part : maps_ws(s.M, s.A).bytes;
+  return (both + 255) / 256 * 256;
+}
+
 }  // namespace
 
 extern "C" {
+
+int moe_linear_adapter_query(const moe_adapter_shape* shape, uint64_t* workspace_bytes) {
+  if (workspace_bytes == nullptr) return MOE_ERR_INVALID;
+  const int rc = check(shape);
+  if (rc != MOE_OK) return rc;
+  *workspace_bytes = adapter_ws(*shape);
+  return MOE_OK;
+}
+
+int moe_linear_adapter_maps(const int32_t* ids_dev, const moe_adapter_shape* shape,
+                            int32_t* offsets_dev, int32_t* row_slot_dev, int32_t* slot_row_dev,
+                            void* workspace_dev, uint64_t workspace_bytes, void* stream) {
+  const int rc = check(shape);
+  if (rc != MOE_OK) return rc;
+  const moe_adapter_shape& s = *shape;
+  if (offsets_dev == nullptr || !aligned(offsets_dev, 4) || !aligned(ids_dev, 4) || !aligned(row_slot_dev, 4) ||
+      !aligned(slot_row_dev, 4))
+    return MOE_ERR_INVALID;
+  if (s.M > 0 && (ids_dev == nullptr || row_slot_dev == nullptr || slot_row_dev == nullptr)) return MOE_ERR_INVALID;
+  const int64_t map = int64_t{4} * s.M;
+  const MapsWs ws = maps_ws(s.M, s.A);
+  const Range ids[1] = {{ids_dev, map}};
+  const Range maps[3] = {{offsets_dev, (int64_t{s.A} + 1) * 4}, {row_slot_dev, map}, {slot_row_dev, map}};
+  if (meet(maps, ids)) return MOE_ERR_INVALID;
+  if (workspace_dev == nullptr || !aligned(workspace_dev, 256) || workspace_bytes < ws.bytes) return MOE_ERR_WORKSPACE;
+  const Range work[1] = {{workspace_dev, static_cast<int64_t>(ws.bytes)}};
+  if (meet(work, ids) || meet(work, maps)) return MOE_ERR_INVALID;
+  DispatchArgs a{};
+  a.ids = ids_dev;
+  a.T = s.M;
+  a.E = s.A;
+  a.topk = 1;
+  a.offsets = offsets_dev;
+  a.row_slot = row_slot_dev;
+  a.slot_row = slot_row_dev;
+  a.range_counts = static_cast<int32_t*>(workspace_dev);
+  a.counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace_dev) + ws.counts);
+  return status(launch_dispatch(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_linear_adapter(const void* x_dev, const int32_t* offsets_dev, const int32_t* row_slot_dev,
+                       const int32_t* slot_row_dev, const void* a_dev, const void* b_dev,
+                       const float* scale_dev, const moe_adapter_shape* shape, const void* base_dev,
+                       void* out_dev, void* workspace_dev, uint64_t workspace_bytes, void* stream) {
+  const int rc = check(shape);
+  if (rc != MOE_OK || shape->M == 0) return rc;
+  const moe_adapter_shape& s = *shape;
+  if (x_dev == nullptr || offsets_dev == nullptr || row_slot_dev == nullptr || slot_row_dev == nullptr ||
+      a_dev == nullptr || b_dev == nullptr || out_dev == nullptr)
+    return MOE_ERR_INVALID;
+  const int64_t so = size_of(s.out_dtype);
+  if (!aligned(x_dev, 16) || !aligned(a_dev, 16) || !aligned(b_dev, 16) || !aligned(offsets_dev, 4) ||
+      !aligned(row_slot_dev, 4) || !aligned(slot_row_dev, 4) || !aligned(scale_dev, 4) ||
+      !aligned(base_dev, static_cast<uintptr_t>(so)) || !aligned(out_dev, static_cast<uintptr_t>(so)))
+    return MOE_ERR_INVALID;
+  const int64_t ldx = s.ldx != 0 ? s.ldx : s.K, ldb = s.ldb != 0 ? s.ldb : s.N, ldo = s.ldo != 0 ? s.ldo : s.N;
+  const int64_t M = s.M, N = s.N, A = s.A, R = s.R;
+  const Range out = {out_dev, ((M - 1) * ldo + N) * so};
+  const Range ins[6] = {{offsets_dev, (A + 1) * 4}, {row_slot_dev, M * 4}, {slot_row_dev, M * 4},
+                        {a_dev, A * R * s.K * 2},   {b_dev, A * N * R * 2}, {scale_dev, A * 4}};
+  const Range rows[2] = {{x_dev, ((M - 1) * ldx + s.K) * 2}, {base_dev, ((M - 1) * ldb + N) * so}};
+  const Range outs[1] = {out};
+  if (meet(outs, ins) || rows_overlap(x_dev, int64_t{s.K} * 2, ldx * 2, out_dev, N * so, ldo * so, M)) return MOE_ERR_INVALID;
+  const bool same = base_dev == out_dev && ldb == ldo;
+  if (base_dev != nullptr && !same && rows_overlap(base_dev, N * so, ldb * so, out_dev, N * so, ldo * so, M))
+    return MOE_ERR_INVALID;
+  const int splits = adapter_splits(M, A, s.K);
+  const int64_t bytes = splits * M * R * 4;
+  if (workspace_dev == nullptr || !aligned(workspace_dev, 256) || workspace_bytes < static_cast<uint64_t>(bytes))
+    return MOE_ERR_WORKSPACE;
+  const Range work[1] = {{workspace_dev, bytes}};
+  if (meet(work, ins) || meet(work, rows) || meet(work, outs)) return MOE_ERR_INVALID;
+  AdapterArgs a{};
+  a.x = x_dev;
+  a.offsets = offsets_dev;
+  a.row_slot = row_slot_dev;
+  a.slot_row = slot_row_dev;
+  a.a = a_dev;
+  a.b = b_dev;
+  a.scale = scale_dev;
+  a.base = base_dev;
+  a.out = out_dev;
+  a.part = static_cast<float*>(workspace_dev);
+  a.M = s.M;
+  a.N = s.N;
+  a.K = s.K;
+  a.R = s.R;
+  a.A = s.A;
+  a.splits = splits;
+  a.dtype = s.dtype;
+  a.out_dtype = s.out_dtype;
+  a.ldx = ldx;
+  a.ldb = ldb;
+  a.ldo = ldo;
+  return status(launch_adapter(a, static_cast<hipStream_t>(stream)));
+}
 
 int moe_linear_grouped(const void* x_dev, const int32_t* offsets_dev, const void* w_dev,
                        const moe_linear_shape* shape, void* out_dev, void* stream) {

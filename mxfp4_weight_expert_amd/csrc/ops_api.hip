@@ -26,18 +26,6 @@ int check(const moe_ops_dispatch_shape* s) {
   return MOE_OK;
 }
 
-struct DispatchWs {
-  uint64_t counts, bytes;  // range counts at 0
-};
-DispatchWs dispatch_ws(const moe_ops_dispatch_shape& s) {
-  const uint64_t slots = static_cast<uint64_t>(s.T) * s.topk;
-  if (slots <= static_cast<uint64_t>(kFusedSlots)) return {0, 256};
-  const uint64_t len = map_range_slots(static_cast<int64_t>(slots));
-  const uint64_t ranges = (slots + len - 1) / len;
-  const uint64_t counts = (ranges * s.E * 4 + 255) / 256 * 256;
-  return {counts, counts + (static_cast<uint64_t>(s.E) * 4 + 255) / 256 * 256};
-}
-
 // Bytes of the token and slot arrays of a shape.
 struct Extents {
   int64_t tokens, rows, map;
@@ -155,7 +143,7 @@ int moe_ops_dispatch_query(const moe_ops_dispatch_shape* shape, uint64_t* worksp
   if (workspace_bytes == nullptr) return MOE_ERR_INVALID;
   const int rc = check(shape);
   if (rc != MOE_OK) return rc;
-  *workspace_bytes = dispatch_ws(*shape).bytes;
+  *workspace_bytes = maps_ws(static_cast<uint64_t>(shape->T) * shape->topk, shape->E).bytes;
   return MOE_OK;
 }
 
@@ -190,7 +178,7 @@ int moe_ops_dispatch(const void* x_dev, const int32_t* topk_ids_dev,
         if (meet(out[i], out[j])) return MOE_ERR_INVALID;
     }
   }
-  const DispatchWs ws = dispatch_ws(s);
+  const MapsWs ws = maps_ws(static_cast<uint64_t>(s.T) * s.topk, s.E);
   if (workspace_dev == nullptr || !aligned(workspace_dev, 256) || workspace_bytes < ws.bytes)
     return MOE_ERR_WORKSPACE;
   const Range work = {workspace_dev, static_cast<int64_t>(ws.bytes)};

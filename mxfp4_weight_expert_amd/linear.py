@@ -16,10 +16,10 @@ import ctypes
 import functools
 from dataclasses import dataclass
 
-from . import ACTIVATION, load_library, ops
+from . import ACTIVATION, MOE_OK, MoeError, load_library, ops
 from .ops import DTYPE, _check, _Kept, _on_stream, _row_stride, _torch_dtype, _whole
 
-__all__ = ["LinearShape", "GatedShape", "grouped_linear", "grouped_linear_backward", "gated_linear",
+__all__ = ["LinearShape", "GatedShape", "AdapterShape", "adapter_query", "adapter_maps", "adapter_linear", "grouped_linear", "grouped_linear_backward", "gated_linear",
            "gated_linear_backward"]
 
 
@@ -32,6 +32,11 @@ class _GatedShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "I", "H", "E", "dtype", "activation")] + [
         (n, ctypes.c_float) for n in ("swiglu_limit", "act_beta", "act_linear_beta")] + [
         ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class _AdapterShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "R", "A", "dtype", "out_dtype")] + [
+        (n, ctypes.c_int64) for n in ("ldx", "ldb", "ldo")]
 
 
 @dataclass(frozen=True)
@@ -101,16 +106,58 @@ class GatedShape(_Kept):
         return (self.M, self.H), (self.M, self.I), (self.M, 2 * self.I), (self.E, 2 * self.I, self.H)
 
 
+@dataclass(frozen=True)
+class AdapterShape(_Kept):
+    """Shape of the adapters' product (fields as in moe_adapter_shape; the row
+    strides come from the tensors). out_dtype None: dtype."""
+
+    M: int
+    N: int
+    K: int
+    R: int
+    A: int
+    dtype: str = "bf16"
+    out_dtype: str = None
+    _sizes = ("M", "N", "K", "R", "A")
+
+    def to_c(self, ldx: int = 0, ldb: int = 0, ldo: int = 0) -> _AdapterShape:
+        self._fits
+        return _AdapterShape(self.M, self.N, self.K, self.R, self.A, DTYPE[self.dtype],
+                             DTYPE[self.out_dtype or self.dtype], ldx, ldb, ldo)
+
+    @functools.cached_property
+    def _c(self):
+        return ctypes.byref(self.to_c())
+
+    @functools.cached_property
+    def _torch(self):
+        return _torch_dtype(self.dtype), _torch_dtype(self.out_dtype or self.dtype)
+
+    @functools.cached_property
+    def _arrays(self):
+        """Shapes of x, out, a, b and the maps."""
+        return ((self.M, self.K), (self.M, self.N), (self.A, self.R, self.K), (self.A, self.N, self.R),
+                (self.A + 1,), (self.M,), (self.A,))
+
+    @functools.cached_property
+    def _workspace(self) -> int:
+        return adapter_query(self)
+
+
 @functools.lru_cache(maxsize=None)
 def _entry(name: str):
     vp = ctypes.c_void_p
-    ls, gs = ctypes.POINTER(_LinearShape), ctypes.POINTER(_GatedShape)
+    ls, gs, ads = (ctypes.POINTER(c) for c in (_LinearShape, _GatedShape, _AdapterShape))
+    u64 = ctypes.c_uint64
     fn = getattr(load_library(), "moe_linear_" + name)
     fn.argtypes = {
         "grouped": [vp, vp, vp, ls, vp, vp],
         "grouped_backward": [vp, vp, vp, vp, ls, vp, vp, vp],
         "gated": [vp, vp, vp, gs, vp, vp, vp],
-        "gated_backward": [vp, vp, vp, vp, vp, gs, vp, vp, vp, vp]}[name]
+        "gated_backward": [vp, vp, vp, vp, vp, gs, vp, vp, vp, vp],
+        "adapter_query": [ads, ctypes.POINTER(u64)],
+        "adapter_maps": [vp, ads, vp, vp, vp, vp, u64, vp],
+        "adapter": [vp, vp, vp, vp, vp, vp, vp, ads, vp, vp, vp, u64, vp]}[name]
     fn.restype = ctypes.c_int
     return fn
 
@@ -236,3 +283,79 @@ def gated_linear_backward(dh, x, offsets, gu, w13, shape: GatedShape, *, dx=None
          None if dx is None else _check(dx, "dx", rows, dt, gpu), None if dw is None else _matrices(dw, "dw", matrices, dt, gpu))
     ops._changed(tuple(t for t in (dgu, dx, dw) if t is not None))
     return dx, dw
+
+
+def adapter_query(shape: AdapterShape) -> int:
+    """Workspace bytes of adapter_maps and adapter_linear for a shape (raises MoeError
+    if unsupported)."""
+    n = ctypes.c_uint64()
+    rc = _entry("adapter_query")(shape._c, ctypes.byref(n))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_linear_adapter_query")
+    return int(n.value)
+
+
+def _workspace(workspace, nbytes: int, like):
+    if workspace is None:
+        workspace = ops.torch.empty(nbytes, dtype=ops.torch.uint8, device=like.device)
+    return workspace, _whole(workspace, "workspace", workspace.shape, ops.torch.uint8, like.get_device())
+
+
+def adapter_maps(ids, shape: AdapterShape, *, offsets=None, row_slot=None, slot_row=None, workspace=None, stream=None):
+    """Rows sorted by adapter; returns (offsets, row_slot, slot_row) for every
+    adapter_linear with the same ids.
+
+    ids int32 [M]: a row's adapter, any value outside [0, A) for none. offsets
+    int32 [A + 1], row_slot (sorted row -> row) and slot_row (row -> sorted row,
+    or -1) int32 [M]. workspace: uint8, at least adapter_query(shape) bytes.
+    """
+    nbytes = shape._workspace
+    if stream is not None:
+        with _on_stream(stream, ids):
+            return adapter_maps(ids, shape, offsets=offsets, row_slot=row_slot, slot_row=slot_row, workspace=workspace)
+    shape._torch  # imports torch
+    *_, bounds, rows, _ = shape._arrays
+    gpu, i32 = ids.get_device(), ops.torch.int32
+    pi = _whole(ids, "ids", rows, i32, gpu)
+    made = [ops.torch.empty(s, dtype=i32, device=ids.device) if t is None else t
+            for t, s in ((offsets, bounds), (row_slot, rows), (slot_row, rows))]
+    workspace, pw = _workspace(workspace, nbytes, ids)
+    _run("adapter_maps", gpu, pi, shape._c, _whole(made[0], "offsets", bounds, i32, gpu),
+         _whole(made[1], "row_slot", rows, i32, gpu), _whole(made[2], "slot_row", rows, i32, gpu), pw, workspace.numel())
+    ops._changed(tuple(made))
+    return tuple(made)
+
+
+def adapter_linear(x, offsets, row_slot, slot_row, a, b, scale, shape: AdapterShape, *, base=None, out=None, workspace=None,
+                   stream=None):
+    """out[m] = base[m] + scale[i] * b[i] @ (a[i] @ x[m]), i the adapter of row m;
+    rows without one get base[m].
+
+    x [M, K] in shape.dtype (rows may be strided, multiples of 8 elements); the
+    maps as adapter_maps returns them; a [A, R, K], b [A, N, R]; scale float32 [A]
+    or None: 1. base [M, N] in shape.out_dtype, or None: 0; out [M, N] may be base
+    itself (rows of both may be strided). workspace: uint8, at least
+    adapter_query(shape) bytes.
+    """
+    (dt, odt), nbytes = shape._torch, shape._workspace
+    if stream is not None:
+        with _on_stream(stream, x):
+            return adapter_linear(x, offsets, row_slot, slot_row, a, b, scale, shape, base=base, out=out, workspace=workspace)
+    rows, result, down, up, bounds, maps, scales = shape._arrays
+    gpu, i32 = x.get_device(), ops.torch.int32
+    ldx, ldb = _row_stride(x, "x", rows, dt, gpu), 0
+    if base is not None:
+        ldb = _row_stride(base, "base", result, odt, gpu)
+    if out is None:
+        out, ldo = ops.torch.empty(result, dtype=odt, device=x.device), 0
+    else:
+        ldo = ldb if out is base else _row_stride(out, "out", result, odt, gpu)
+    workspace, pw = _workspace(workspace, nbytes, x)
+    _run("adapter", gpu, x.data_ptr(), _whole(offsets, "offsets", bounds, i32, gpu),
+         _whole(row_slot, "row_slot", maps, i32, gpu), _whole(slot_row, "slot_row", maps, i32, gpu),
+         _check(a, "a", down, dt, gpu), _check(b, "b", up, dt, gpu),
+         None if scale is None else _check(scale, "scale", scales, ops.torch.float32, gpu),
+         ctypes.byref(shape.to_c(ldx, ldb, ldo)) if ldx or ldb or ldo else shape._c,
+         None if base is None else base.data_ptr(), out.data_ptr(), pw, workspace.numel())
+    ops._changed((out,))
+    return out
