@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_mxfp4.so")
 SOURCES = ["api.hip", "route.hip", "sort.hip", "quant.hip", "gemm.hip", "gemm_tiled.hip",
            "finalize.hip", "pack.hip", "dispatch.hip", "combine.hip", "w4_bf16.hip", "w4_fp16.hip", "ops_api.hip",
-           "tile_forward.hip", "tile_backward.hip", "act_grad.hip", "adapter.hip", "linear_api.hip"]
+           "few_rows.hip", "tile_forward.hip", "tile_backward.hip", "act_grad.hip", "adapter.hip", "linear_api.hip"]
 ARCH = "gfx950"
 JOBS = 6  # sources compiled at once
 

@@ -170,6 +170,7 @@ struct TileArgs {
   ActArgs act;             // gated
 };
 hipError_t launch_tile_forward(const TileArgs& a, bool gated, hipStream_t st);
+hipError_t launch_few_rows(const TileArgs& a, bool gated, hipStream_t st);  // forward (few_rows.hip)
 hipError_t launch_tile_row_grad(const TileArgs& a, hipStream_t st);
 hipError_t launch_tile_mat_grad(const TileArgs& a, hipStream_t st);
 

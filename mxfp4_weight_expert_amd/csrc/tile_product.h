@@ -1,4 +1,4 @@
-// Products of 16-bit matrices in tiles of 256 x 256 on the matrix cores, one
+// Products of 16-bit matrices in square tiles on the matrix cores, one
 // kernel for the forward pass and both gradients of rows times their expert's
 // matrix (offsets given) or one matrix for all rows (offsets null):
 //
@@ -8,7 +8,7 @@
 //
 // Each is out[c, r] = sum over i of P[r, i] Q[c, i], r the side whose elements
 // follow each other in out. P is the A operand of the 32x32x16 MFMA and Q its B
-// operand, so a lane has 16 consecutive elements of out:
+// operand, so a lane has four neighbours of a row of out at a time:
 //
 //              r  c  i    P             Q
 //   kForward   n  m  k    w, i inner    x, i inner
@@ -16,13 +16,16 @@
 //   kMatGrad   k  n  m    x, r inner    dout, c inner
 //
 // Operands whose inner index is i go to LDS as rows of 64 bytes (32 i) and are
-// read 16 bytes a lane. The others go as 32 rows of 512 bytes, and the transposing
+// read 16 bytes a lane. The others go as 32 rows of the tile's width, and the transposing
 // LDS read (ds_read_b64_tr_b16: within 16 lanes, lane 4 a + b gives four columns
 // 4 b of row a, and lane j receives column j of the four rows) makes the operand.
 #pragma once
 
 #include "rows.h"
 #include "kernels.h"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
@@ -32,13 +35,16 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 enum { kForward, kRowGrad, kMatGrad };
 
-constexpr int kTile = 256;              // both sides of a tile
-constexpr int kStep = 32;               // i of a stage
-constexpr int kSide = kTile * kStep * 2;  // bytes of one operand's stage (16 KB)
-constexpr int kStage = 2 * kSide;
-constexpr int kSlots = 4;               // stages in LDS: one read, up to three in flight
-constexpr int kTileThreads = 512;
-constexpr int kStageLoads = kStage / 1024 / (kTileThreads / 64);  // a wave's, of 1 KB
+constexpr int kStep = 32;      // i of a stage
+constexpr int kSlots = 4;      // stages in LDS: one read, up to three in flight
+constexpr int PB = 2;          // 32-blocks of r of a wave
+// Tiles of T x T. T = 256, 128: T / 32 waves, each with 64 r and every second 32 c, share
+// the stages. T = 64: four waves take every fourth stage each, with stages of their own
+// and no barrier between them, and join their sums at the end.
+constexpr int tile_split(int T) { return T == 64 ? 4 : 1; }
+constexpr int tile_threads(int T) { return T == 64 ? 256 : T * 2; }
+constexpr int tile_stage(int T) { return 2 * T * kStep * 2; }  // bytes of both operands
+constexpr int tile_lds(int T) { return kSlots * tile_stage(T) * tile_split(T); }
 
 template <int DT>
 __device__ __forceinline__ f32x16_t mfma32(uint4 a, uint4 b, f32x16_t c) {
@@ -60,32 +66,32 @@ __device__ __forceinline__ void load_to_lds(uint64_t base, uint32_t off, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(rsrc)
-               : "memory", "m0");
+               : "memory");  // compiled code sets m0 right before each of its own uses
 }
 
-// Rows of 64 bytes: 16-byte chunk c of row r lies at chunk c ^ chunk_swz(r), so
-// that 16 rows of a multiple of 16, and 32 of a multiple of 32, read at one chunk
-// fall on different banks.
-__device__ __forceinline__ uint32_t chunk_swz(uint32_t r) { return (r >> 3 & 1) * 2 + ((r >> 2 ^ r >> 4) & 1); }
-// Rows of 512 bytes: 64-byte piece g of row r lies at piece g ^ piece_swz(r): the four
-// rows of a transposing read, and those of its other half eight further on, fall on
+// Rows of 64 bytes: 16-byte chunk c of row r lies at chunk c ^ chunk_swz(r). LDS serves
+// a 16-byte read sixteen lanes at a time, in groups of four neighbours: 0, 12, 20 and 24
+// on, then 4, 8, 16 and 28 on; the four chunks of these rows are different ones (no
+// conflicts; counted).
+__device__ __forceinline__ uint32_t chunk_swz(uint32_t r) { return r >> 2 & 3; }
+// Rows of 512, 256 or 128 bytes: 64-byte piece g of row r lies at piece g ^ piece_swz(r): the
+// four rows of a transposing read, and those of its other half eight further on, fall on
 // different banks.
-__device__ __forceinline__ uint32_t piece_swz(uint32_t r) { return (r & 3) | (r >> 3 & 1) << 2; }
-
-// The r of tile row rho of P (0..255), from the tile's first. In a 32-row block the
-// MFMA gives a lane rows 8 b + 4 h + i (h its half, registers 4 b + i): they stand
-// for r = 16 h + 4 b + i, the lane's registers in order. Gated: registers 0..7 are
-// gate rows and 8..15 up rows of the same eight features.
-__device__ __forceinline__ uint32_t plain_row(uint32_t rho) {
-  const uint32_t b = rho >> 3 & 3, h = rho >> 2 & 1, i = rho & 3;
-  return (rho & ~31u) + 16 * h + 4 * b + i;
+template <int T>
+__device__ __forceinline__ uint32_t piece_swz(uint32_t r) {
+  return T == 256 ? (r & 3) | (r >> 3 & 1) << 2 : T == 128 ? (r & 3) ^ (r >> 3 & 1) : r >> 1 & 1;
 }
-__device__ __forceinline__ uint32_t gated_feature(uint32_t rho) {
-  const uint32_t b = rho >> 3 & 1, h = rho >> 2 & 1, i = rho & 3;
-  return (rho >> 5) * 16 + 8 * h + 4 * b + i;
-}
-__device__ __forceinline__ bool gated_up(uint32_t rho) { return (rho >> 4 & 1) != 0; }
 
+// Gated: a wave's first 32-block of r are gate rows, the second the up rows of the same
+// features, which so meet in a lane.
+__device__ __forceinline__ uint32_t gated_feature(uint32_t rho) { return (rho >> 6) * 32 + (rho & 31); }
+__device__ __forceinline__ bool gated_up(uint32_t rho) { return (rho >> 5 & 1) != 0; }
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT == MOE_DTYPE_BF16) return pack_bf16x2(lo, hi);
+  else return Row<MOE_DTYPE_FP16>::pack2(lo, hi);
+}
 // One tile of out.
 struct TileItem {
   int e;      // matrix
@@ -96,26 +102,35 @@ struct TileItem {
   int len;    // i to sum over
 };
 
-template <int MODE, bool GATED, int DT>
-__global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs a) {
+template <int T, int MODE, bool GATED, int DT>
+__global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product_kernel(TileArgs a) {
   static_assert(!GATED || MODE == kForward, "the activation follows the forward product");
   constexpr bool kPInner = MODE == kForward;   // i is P's inner index
   constexpr bool kQInner = MODE != kMatGrad;
-  constexpr int kWide = GATED ? kTile / 2 : kTile;  // r of a tile
-  constexpr int PB = 2, NQ = 4;                     // 32-blocks of a wave: r, c
+  constexpr int kWide = GATED ? T / 2 : T;      // r of a tile
+  constexpr int KW = tile_split(T), WC = KW > 1 ? 1 : 2;  // waves along i, along c
+  constexpr int NQ = T / (32 * WC);               // 32-blocks of c of a wave: every WC-th
+  constexpr int kThreads = tile_threads(T), kWaves = kThreads / 64, kStage = tile_stage(T), kSide = kStage / 2;
+  constexpr int kLoads = kSide / 1024 / (KW > 1 ? 1 : kWaves);  // a wave's loads of 1 KB of an operand's stage
+  constexpr int kRow = 2 * T;                     // bytes of a row whose inner index is not i
   extern __shared__ __attribute__((aligned(1024))) uint8_t s_dyn[];
-  __shared__ int32_t s_wave[kTileThreads / 64];
-  int32_t* const s_first = reinterpret_cast<int32_t*>(s_dyn + kSlots * kStage);  // grouped: tiles before each expert
+  __shared__ int32_t s_wave[kWaves];
+  int32_t* const s_first = reinterpret_cast<int32_t*>(s_dyn + tile_lds(T));  // grouped: tiles before each expert
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)s_dyn));
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_index();
-  const int wr = wv & 3, wc = wv >> 2;  // wave: 64 r, and every second 32 c
+  constexpr int kAlong = T / (32 * PB);  // waves along r
+  const int wr = wv % kAlong, wc = KW > 1 ? 0 : wv / kAlong;
+  const int part = KW > 1 ? wv : 0, lw = KW > 1 ? 0 : wv;      // of the stages; of a stage's loads
+  const uint32_t of_wave = KW > 1 ? wv * kSlots * kStage : 0;
+  uint8_t* const ring = s_dyn + of_wave;
+  const uint32_t ring0 = lds0 + of_wave;
   const int nr = (a.R + kWide - 1) / kWide;
 
   // The tiles of the experts' rows.
-  int tiles = (a.M + kTile - 1) / kTile;
+  int tiles = (a.M + T - 1) / T;
   if (MODE != kMatGrad && a.offsets != nullptr) {
-    constexpr int kPer = kMaxExperts / kTileThreads;
+    constexpr int kPer = kMaxExperts / kThreads;
     int n[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -123,7 +138,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       n[i] = 0;
       if (e < a.E) {
         const int lo = min(max(a.offsets[e], 0), a.M), hi = min(a.offsets[e + 1], a.M);
-        n[i] = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
+        n[i] = hi > lo ? (hi - lo + T - 1) / T : 0;
       }
       sum += n[i];
     }
@@ -132,7 +147,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
     __syncthreads();
     int at = incl - sum;
     tiles = 0;
-    for (int i = 0; i < kTileThreads / 64; ++i) {
+    for (int i = 0; i < kWaves; ++i) {
       if (i < wv) at += s_wave[i];
       tiles += s_wave[i];
     }
@@ -142,19 +157,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       if (e <= a.E) s_first[e] = at;
       at += n[i];
     }
-    if (a.E == kMaxExperts && tid == kTileThreads - 1) s_first[kMaxExperts] = at;
+    if (a.E == kMaxExperts && tid == kThreads - 1) s_first[kMaxExperts] = at;
     __syncthreads();
     tiles = __builtin_amdgcn_readfirstlane(tiles);
   }
-  const int nc = (a.C + kTile - 1) / kTile;  // kMatGrad: tiles along dout's columns
+  const int nc = (a.C + T - 1) / T;  // kMatGrad: tiles along dout's columns
   const int items = static_cast<int>(min(
       MODE == kMatGrad ? static_cast<int64_t>(a.E) * nc * nr : static_cast<int64_t>(tiles) * nr, kMaxTileItems));
 
-  // The blocks of an XCD (block ids go round over the eight) walk a range of the
-  // items together, so that neighbours, which share operands, meet in its L2.
-  const int per = (items + 7) >> 3, walkers = static_cast<int>(gridDim.x) >> 3;
-  const int xcd = blockIdx.x & 7, last = min(items, (xcd + 1) * per);
-  const int item0 = xcd * per + (blockIdx.x >> 3);
+  // The item of a block's round k. In a round the blocks of an XCD (block ids go round
+  // over the eight) take neighbours, which share operands and meet in its L2. One matrix:
+  // each XCD has a range of its own, so that it meets them in the next round too. Experts,
+  // whose tiles cost differently: the XCDs take turns (64 experts of 256 rows 1382 us,
+  // 1512 with ranges; one matrix the other way 950 and 912).
+  const int walkers = static_cast<int>(gridDim.x) >> 3, xcd = blockIdx.x & 7, walker = blockIdx.x >> 3;
+  const int per = (items + 7) >> 3;
+  auto item_of = [&](int k) {
+    const int at = k * walkers + walker;
+    if (a.offsets == nullptr) return at < per ? xcd * per + at : items;
+    return k * static_cast<int>(gridDim.x) + xcd * walkers + walker;
+  };
 
   auto decode = [&](int item) {
     TileItem t;
@@ -162,8 +184,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       const int re = item / nr, e = re / nc;
       t.e = e;
       t.r0 = (item - re * nr) * kWide;
-      t.c0 = (re - e * nc) * kTile;
-      t.cols = min(kTile, a.C - t.c0);
+      t.c0 = (re - e * nc) * T;
+      t.cols = min(T, a.C - t.c0);
       int lo = 0, hi = a.M;
       if (a.offsets != nullptr) {
         lo = min(max(a.offsets[e], 0), a.M);
@@ -190,22 +212,25 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       }
       t.e = e;
       t.r0 = r * kWide;
-      t.c0 = lo + local * kTile;
-      t.cols = min(kTile, hi - t.c0);
+      // the expert's tiles of one size, a multiple of 32: full tiles with a short last one
+      // cost more, and unequal shares (64 experts of 256 rows on average 1395 us, 1497)
+      const int n = (hi - lo + T - 1) / T, width = ((hi - lo + n - 1) / n + 31) & ~31;
+      t.c0 = lo + local * width;
+      t.cols = min(width, hi - t.c0);
       t.first = 0;
       t.len = a.I;
     }
     return t;
   };
 
-  // ---- loads. A wave brings 2 KB of each operand: 32 rows of 64 bytes, or 4 of 512.
-  int l_item = item0, l_left = 0;  // i left of the item that loads come from
+  // ---- loads
+  int l_round = 0, l_left = 0;     // the item that loads come from: its round, its i left
   uint64_t pbase = 0, qbase = 0;   // where the next stage begins
-  uint32_t poff[2], qoff[2];
-  uint32_t pi[2], qi[2];           // the lane's i in a stage
+  uint32_t poff[kLoads], qoff[kLoads];
+  uint32_t pi[kLoads], qi[kLoads];           // the lane's i in a stage
   auto start = [&]() {
-    const TileItem t = decode(l_item);
-    l_left = t.len;
+    const TileItem t = decode(item_of(l_round));
+    l_left = t.len - part * kStep;
     pbase = reinterpret_cast<uint64_t>(a.p);
     qbase = reinterpret_cast<uint64_t>(a.q);
     if constexpr (MODE == kMatGrad)
@@ -214,31 +239,32 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       pbase += (static_cast<uint64_t>(t.e) * a.pstride + static_cast<uint64_t>(t.r0) * a.ldp) * 2;
     else
       pbase += (static_cast<uint64_t>(t.e) * a.pstride + t.r0) * 2;
+    pbase += static_cast<uint64_t>(part) * (kPInner ? kStep * 2 : a.ldp * (kStep * 2));
+    qbase += static_cast<uint64_t>(part) * (kQInner ? kStep * 2 : a.ldq * (kStep * 2));
     qbase += (MODE == kMatGrad ? static_cast<uint64_t>(t.first) * a.ldq + t.c0
                                : static_cast<uint64_t>(t.c0) * a.ldq) * 2;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kLoads; ++j) {
+      // a load of rows whose inner index is not i: two rows of 512 bytes, four of 256, eight of 128
+      const uint32_t row = (lw * kLoads + j) * (1024 / kRow) + lane / (kRow / 16);
+      const uint32_t across = ((lane / 4 % (kRow / 64)) ^ piece_swz<T>(row)) * 4 + (lane & 3);  // 16-byte chunk
       if constexpr (kPInner) {
-        const uint32_t rho = wv * 32 + j * 16 + (lane >> 2), chunk = (lane & 3) ^ chunk_swz(rho);
-        const uint32_t r = GATED ? gated_feature(rho) : plain_row(rho);
+        const uint32_t rho = (lw * kLoads + j) * 16 + (lane >> 2), chunk = (lane & 3) ^ chunk_swz(rho);
+        const uint32_t r = GATED ? gated_feature(rho) : rho;
         const bool in = t.r0 + r < static_cast<uint32_t>(a.R);
         poff[j] = in ? (r + (GATED && gated_up(rho) ? a.R : 0)) * static_cast<uint32_t>(a.ldp) * 2 + chunk * 16 : kNoRow;
         pi[j] = chunk * 8;
       } else {
-        const uint32_t row = wv * 4 + j * 2 + (lane >> 5);
-        const uint32_t chunk = ((lane >> 2 & 7) ^ piece_swz(row)) * 4 + (lane & 3);
-        const bool in = t.r0 + chunk * 8 < static_cast<uint32_t>(a.R);
-        poff[j] = in ? row * static_cast<uint32_t>(a.ldp) * 2 + chunk * 16 : kNoRow;
+        const bool in = t.r0 + across * 8 < static_cast<uint32_t>(a.R);
+        poff[j] = in ? row * static_cast<uint32_t>(a.ldp) * 2 + across * 16 : kNoRow;
         pi[j] = row;
       }
       if constexpr (kQInner) {
-        const uint32_t c = wv * 32 + j * 16 + (lane >> 2), chunk = (lane & 3) ^ chunk_swz(c);
+        const uint32_t c = (lw * kLoads + j) * 16 + (lane >> 2), chunk = (lane & 3) ^ chunk_swz(c);
         qoff[j] = c < static_cast<uint32_t>(t.cols) ? c * static_cast<uint32_t>(a.ldq) * 2 + chunk * 16 : kNoRow;
         qi[j] = chunk * 8;
       } else {
-        const uint32_t row = wv * 4 + j * 2 + (lane >> 5);
-        const uint32_t chunk = ((lane >> 2 & 7) ^ piece_swz(row)) * 4 + (lane & 3);
-        qoff[j] = chunk * 8 < static_cast<uint32_t>(t.cols) ? row * static_cast<uint32_t>(a.ldq) * 2 + chunk * 16 : kNoRow;
+        qoff[j] = across * 8 < static_cast<uint32_t>(t.cols) ? row * static_cast<uint32_t>(a.ldq) * 2 + across * 16 : kNoRow;
         qi[j] = row;
       }
     }
@@ -246,72 +272,79 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
   // The next stage into slot `slot`; past the last item loads that touch no memory, so
   // that the waits count the same everywhere.
   auto issue = [&](int slot) {
-    while (l_left <= 0 && l_item < last) {
-      l_item += walkers;
-      if (l_item < last) start();
+    while (l_left <= 0 && item_of(l_round) < items) {
+      ++l_round;
+      if (item_of(l_round) < items) start();
     }
-    const uint32_t at = lds0 + slot * kStage + wv * 2048;
+    const uint32_t left = max(l_left, 0), at = ring0 + slot * kStage + lw * kLoads * 1024;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      load_to_lds(pbase, pi[j] < static_cast<uint32_t>(max(l_left, 0)) ? poff[j] : kNoRow, at + j * 1024);
-      load_to_lds(qbase, qi[j] < static_cast<uint32_t>(max(l_left, 0)) ? qoff[j] : kNoRow, at + kSide + j * 1024);
+    for (int j = 0; j < kLoads; ++j) {
+      load_to_lds(pbase, pi[j] < left ? poff[j] : kNoRow, at + j * 1024);
+      load_to_lds(qbase, qi[j] < left ? qoff[j] : kNoRow, at + kSide + j * 1024);
     }
-    pbase += kPInner ? kStep * 2 : static_cast<uint64_t>(a.ldp) * (kStep * 2);
-    qbase += kQInner ? kStep * 2 : static_cast<uint64_t>(a.ldq) * (kStep * 2);
-    l_left -= kStep;
+    pbase += kPInner ? KW * kStep * 2 : static_cast<uint64_t>(a.ldp) * (KW * kStep * 2);
+    qbase += kQInner ? KW * kStep * 2 : static_cast<uint64_t>(a.ldq) * (KW * kStep * 2);
+    l_left -= KW * kStep;
   };
 
-  if (item0 >= last) return;
+  if (item_of(0) >= items) return;
   start();
 #pragma unroll
   for (int s = 0; s < kSlots - 1; ++s) issue(s);
 
   // ---- operands from LDS
   const int l32 = lane & 31, half = lane >> 5;
-  uint32_t pat[2], qat[4];
+  uint32_t pat[kPInner ? 2 : PB], qat[kQInner ? 2 : NQ];
   if constexpr (kPInner) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) pat[s] = (wr * 64 + l32) * 64 + (((2 * s + half) ^ chunk_swz(l32)) << 4);
+    for (int s = 0; s < 2; ++s) pat[s] = (wr * PB * 32 + l32) * 64 + (((2 * s + half) ^ chunk_swz(l32)) << 4);
   } else {
     const uint32_t row = half * 8 + (lane >> 2 & 3), gg = lane >> 4 & 1, q = lane & 3;
-    // columns 4 q of a 16-lane group stand for the rows 16 gg + 4 q of the MFMA
-    const uint32_t b = 2 * gg + (q >> 1), h = q & 1;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) pat[p] = row * 512 + (((wr * 2 + p) ^ piece_swz(row)) << 6) + (4 * h + b) * 8;
+    for (int p = 0; p < PB; ++p) pat[p] = row * kRow + (((wr * PB + p) ^ piece_swz<T>(row)) << 6) + (4 * gg + q) * 8;
   }
   if constexpr (kQInner) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) qat[s] = kSide + (wc * 32 + l32) * 64 + (((2 * s + half) ^ chunk_swz(l32)) << 4);
-    qat[2] = qat[3] = 0;
   } else {
     const uint32_t row = half * 8 + (lane >> 2 & 3), gg = lane >> 4 & 1, q = lane & 3;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) qat[n] = kSide + row * 512 + (((2 * n + wc) ^ piece_swz(row)) << 6) + (4 * gg + q) * 8;
+    for (int n = 0; n < NQ; ++n) qat[n] = kSide + row * kRow + (((WC * n + wc) ^ piece_swz<T>(row)) << 6) + (4 * gg + q) * 8;
   }
   auto transposed = [&](const uint8_t* at) {  // eight i of 32 rows or columns
     typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
     const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at));
-    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * 512));
+    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * kRow));
     const uint2 u = __builtin_bit_cast(uint2, lo), v = __builtin_bit_cast(uint2, hi);
     return uint4{u.x, u.y, v.x, v.y};
   };
   auto read_p = [&](const uint8_t* stage, int s, int b) {
     if constexpr (kPInner) return ld16(stage + pat[s] + b * 32 * 64);
-    else return transposed(stage + pat[b] + s * 16 * 512);
+    else return transposed(stage + pat[b] + s * 16 * kRow);
   };
   auto read_q = [&](const uint8_t* stage, int s, int n) {
-    if constexpr (kQInner) return ld16(stage + qat[s] + n * 64 * 64);
-    else return transposed(stage + qat[n] + s * 16 * 512);
+    if constexpr (kQInner) return ld16(stage + qat[s] + n * WC * 32 * 64);
+    else return transposed(stage + qat[n] + s * 16 * kRow);
+  };
+
+  // Waits until a stage's loads are done: those of the next two stages, and `stores`
+  // stores behind them, may be under way.
+  auto wait_stage = [&](int stores) {
+    constexpr int kAhead = (kSlots - 2) * 2 * kLoads;
+    if (stores >= 32) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead + 32) : "memory");
+    else if (stores >= 16) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead + 16) : "memory");
+    else if (stores >= 8) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead + 8) : "memory");
+    else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead) : "memory");
   };
 
   f32x16_t acc[PB][NQ];
   uint4 p0[PB], q0[NQ], p1[PB], q1[NQ];
-  int slot = 0;
-  for (int item = item0; item < last; item += walkers) {
-    const TileItem t = decode(item);
-    const int stages = (t.len + kStep - 1) / kStep;
+  int slot = 0, stores = 0;
+  for (int round = 0; item_of(round) < items; ++round) {
+    const TileItem t = decode(item_of(round));
+    const int stages = max(0, (t.len - part * kStep + KW * kStep - 1) / (KW * kStep));  // this wave's
     // 32-blocks of c that hold anything, for this wave
-    const int blocks = min(NQ, max(0, (t.cols - 32 * wc + 63) >> 6));
+    const int blocks = min(NQ, max(0, (t.cols - 32 * wc + 32 * WC - 1) / (32 * WC)));
 #pragma unroll
     for (int b = 0; b < PB; ++b)
 #pragma unroll
@@ -323,11 +356,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
     // that stage's first operands are read.
     auto walk = [&](auto nqc) {
       constexpr int N = decltype(nqc)::value;
+      // Half a stage's products from operands in registers, with the LDS reads of the
+      // other half, written before them, between the first.
       auto mul = [&](const uint4 (&p)[PB], const uint4 (&q)[NQ]) {
+        constexpr int kMuls = PB * N, kReads = (kPInner ? PB : 2 * PB) + (kQInner ? N : 2 * N);
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+        for (int i = 0; i < kMuls; ++i)
+          acc[i % PB][i / PB] = mfma32<DT>(p[i % PB], q[i / PB], acc[i % PB][i / PB]);
 #pragma unroll
-          for (int b = 0; b < PB; ++b) acc[b][n] = mfma32<DT>(p[b], q[n], acc[b][n]);
+        for (int i = 0; i < kReads; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+          if (i < kMuls) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // one MFMA
+        }
+        __builtin_amdgcn_sched_barrier(0);
       };
 #pragma unroll
       for (int b = 0; b < PB; ++b) p1[b] = uint4{0, 0, 0, 0};
@@ -336,11 +377,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       for (int k = 0; k < stages; ++k) {
         // this stage has come (three are in flight), and no wave still reads the slot
         // that the next loads go to
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kSlots - 2) * kStageLoads) : "memory");
-        __builtin_amdgcn_s_barrier();
+        // (the stores of the last item's results, younger than three stages' loads, go on)
+        if (k >= kSlots - 1) stores = 0;
+        wait_stage(stores);
+        if constexpr (KW == 1) __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         issue(slot == 0 ? kSlots - 1 : slot - 1);
-        const uint8_t* const stage = s_dyn + slot * kStage;
+        const uint8_t* const stage = ring + slot * kStage;
         if constexpr (N > 0) {
 #pragma unroll
           for (int b = 0; b < PB; ++b) p0[b] = read_p(stage, 0, b);
@@ -358,58 +401,158 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_product_kernel(TileArgs 
       mul(p1, q1);
     };
     switch (blocks) {
-      case 4: walk(std::integral_constant<int, 4>{}); break;
-      case 3: walk(std::integral_constant<int, 3>{}); break;
+      case 4: walk(std::integral_constant<int, NQ>{}); break;
+      case 3: walk(std::integral_constant<int, std::min(NQ, 3)>{}); break;
       case 2: walk(std::integral_constant<int, 2>{}); break;
       case 1: walk(std::integral_constant<int, 1>{}); break;
       default: walk(std::integral_constant<int, 0>{}); break;
     }
 
-    // ---- results: lane (c, h) has 16 r of each 32-block
+    // ---- results: register 4 b + i of lane (l, h) is c = l, r = 8 b + 4 h + i of a
+    // block. They pass through LDS, in the slot of the stage read last, 32 rows of up to
+    // 128 bytes at a time, so that the stores write whole rows of 128 bytes (their 16-byte
+    // pieces, straight from the registers, lie in 64 places: 2102 us where these take 1626
+    // for 64 experts' gradients of 2048 x 7168 in 32 bits).
+    auto meet = [&]() {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    if constexpr (KW == 1) meet();  // no wave still reads that slot
+    uint8_t* const mine = ring + (slot == 0 ? kSlots - 1 : slot - 1) * kStage + lw * 4096;
+    const int64_t row0 = (MODE == kMatGrad ? static_cast<int64_t>(t.e) * a.C : 0) + t.c0;
+    // put(b): eight or sixteen bytes of four neighbours in row l32 of the piece; 16-byte
+    // chunks are swapped so that neither side meets bank conflicts
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // addresses made from it are not kept in registers throughout
+    const int l32 = ln & 31, half = ln >> 5;
+    auto place = [&](int row, int chunk) { return mine + row * 128 + ((chunk ^ (row >> 1 & 7)) << 4); };
+    auto put16 = [&](int col, float x, float y, float z, float w) {
+      *reinterpret_cast<uint2*>(place(l32, col >> 3) + (col & 4) * 2) = uint2{pack2<DT>(x, y), pack2<DT>(z, w)};
+    };
+    auto put32 = [&](int col, float x, float y, float z, float w) {
+      *reinterpret_cast<uint4*>(place(l32, col >> 2)) =
+          uint4{__float_as_uint(x), __float_as_uint(y), __float_as_uint(z), __float_as_uint(w)};
+    };
+    // Rows of BYTES from `mine` to columns [at, ...) of rows [c0, c0 + 32) of the tile; n
+    // elements of `size` bytes of them are columns of out.
+    auto flush = [&](void* to, int64_t ld, int at, int c0, int n, auto bytesc, auto sizec) {
+      constexpr int bytes = decltype(bytesc)::value, size = decltype(sizec)::value, lanes = bytes / 16;
+      uint32_t stride = static_cast<uint32_t>(ld) * size;
+      asm volatile("" : "+s"(stride));
+      const __amdgpu_buffer_rsrc_t rs =
+          make_rsrc(static_cast<uint8_t*>(to) + (row0 * ld + at) * size, static_cast<uint32_t>(t.cols) * stride);
+      __builtin_amdgcn_wave_barrier();
+      const int chunk = ln % lanes;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int c = (2 * n + wc) * 32 + l32;
-      if (c >= t.cols) continue;
-      const int64_t row = (MODE == kMatGrad ? static_cast<int64_t>(t.e) * a.C : 0) + t.c0 + c;
+      for (int i = 0; i < 32 * lanes / 64; ++i) {
+        const int row = i * (64 / lanes) + ln / lanes;
+        const uint32_t off = chunk * (16 / size) < n ? (c0 + row) * stride + chunk * 16 : kNoRow;
+        bst16(rs, c0 + row < t.cols ? off : kNoRow, ld16(place(row, chunk)));
+      }
+      __builtin_amdgcn_wave_barrier();
+    };
+    constexpr std::integral_constant<int, 128> whole{};
+    constexpr std::integral_constant<int, 64> half_row{};
+    constexpr std::integral_constant<int, 32> quarter_row{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, 4> four{};
+    if constexpr (KW > 1) {
+      // Each wave's sums of one c block to its own slot; wave w adds up block w % 2,
+      // registers 8 (w / 2) on of both r blocks: 16 r each.
+      f32x4_t sum[2][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int b = 0; b < PB; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            reinterpret_cast<f32x4_t*>(mine)[(b * 4 + g) * kWave + ln] =
+                f32x4_t{acc[b][n][4 * g], acc[b][n][4 * g + 1], acc[b][n][4 * g + 2], acc[b][n][4 * g + 3]};
+        s_wave[wv] = static_cast<int>(mine - s_dyn);
+        meet();
+        if ((wv & 1) == n) {
+#pragma unroll
+          for (int b = 0; b < PB; ++b)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              sum[b][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int w = 0; w < KW; ++w)
+                sum[b][g] += reinterpret_cast<const f32x4_t*>(s_dyn + s_wave[w])[(b * 4 + (wv >> 1) * 2 + g) * kWave + ln];
+            }
+        }
+        meet();
+      }
+      const int c0 = (wv & 1) * 32, first = t.r0 + (wv >> 1) * 16;
+      if constexpr (GATED) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = act_apply(sum[0][g][i], sum[1][g][i], a.act);
+          put16(g * 8 + half * 4, h[0], h[1], h[2], h[3]);
+        }
+        flush(a.out, a.ldo, first, c0, a.R - first, quarter_row, two);
+      }
 #pragma unroll
       for (int b = 0; b < PB; ++b) {
-        if constexpr (GATED) {
-          const int f = t.r0 + (wr * PB + b) * 16 + half * 8;
-          if (f >= a.R) continue;
-          float h[8];
-          float g[8], u[8];
+        if (GATED && a.gu == nullptr) break;
+        const int r0 = GATED ? first : first + b * 32;
+        const bool wide = !GATED && a.out_dtype == MOE_DTYPE_FP32;
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            g[v] = acc[b][n][v];
-            u[v] = acc[b][n][v + 8];
-            h[v] = act_apply(g[v], u[v], a.act);
-          }
-          uint16_t* const o = static_cast<uint16_t*>(a.out) + row * a.ldo + f;
-          *reinterpret_cast<uint4*>(o) = Row<DT>::pack(h);
-          if (a.gu != nullptr) {
-            uint16_t* const p = static_cast<uint16_t*>(a.gu) + row * 2 * a.R + f;
-            *reinterpret_cast<uint4*>(p) = Row<DT>::pack(g);
-            *reinterpret_cast<uint4*>(p + a.R) = Row<DT>::pack(u);
-          }
-        } else {
-          const int r = t.r0 + (wr * PB + b) * 32 + half * 16;
-          float f[16];
+        for (int g = 0; g < 2; ++g) {
+          if (wide) put32(g * 8 + half * 4, sum[b][g][0], sum[b][g][1], sum[b][g][2], sum[b][g][3]);
+          else put16(g * 8 + half * 4, sum[b][g][0], sum[b][g][1], sum[b][g][2], sum[b][g][3]);
+        }
+        if (GATED) flush(a.gu, 2 * a.R, r0 + b * a.R, c0, a.R - r0, quarter_row, two);
+        else if (wide) flush(a.out, a.ldo, r0, c0, a.R - r0, half_row, four);
+        else flush(a.out, a.ldo, r0, c0, a.R - r0, quarter_row, two);
+      }
+      continue;
+    }
 #pragma unroll
-          for (int v = 0; v < 16; ++v) f[v] = acc[b][n][v];
-          if (a.out_dtype == MOE_DTYPE_FP32) {
-            float* const o = static_cast<float*>(a.out) + row * a.ldo + r;
+    for (int n = 0; n < NQ; ++n) {
+      const int c0 = (WC * n + wc) * 32;
+      if constexpr (GATED) {
+        const int f0 = wr * 32, left = a.R - t.r0 - f0;
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+          float h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = act_apply(acc[0][n][v + i], acc[1][n][v + i], a.act);
+          put16(v * 2 + half * 4, h[0], h[1], h[2], h[3]);
+        }
+        flush(a.out, a.ldo, t.r0 + f0, c0, left, half_row, two);
+        if (a.gu != nullptr) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int v = 0; v < 16; v += 4)
-              if (r + v < a.R) *reinterpret_cast<uint4*>(o + v) = Row<MOE_DTYPE_FP32>::pack(f + v);
-          } else {
-            uint16_t* const o = static_cast<uint16_t*>(a.out) + row * a.ldo + r;
-#pragma unroll
-            for (int v = 0; v < 16; v += 8)
-              if (r + v < a.R) *reinterpret_cast<uint4*>(o + v) = Row<DT>::pack(f + v);
+              put16(v * 2 + half * 4, acc[b][n][v], acc[b][n][v + 1], acc[b][n][v + 2], acc[b][n][v + 3]);
+            flush(a.gu, 2 * a.R, t.r0 + f0 + b * a.R, c0, left, half_row, two);
           }
         }
+      } else if (a.out_dtype == MOE_DTYPE_FP32) {
+#pragma unroll
+        for (int b = 0; b < PB; ++b) {
+          const int r0 = t.r0 + (wr * PB + b) * 32;
+#pragma unroll
+          for (int v = 0; v < 16; v += 4)
+            put32(v * 2 + half * 4, acc[b][n][v], acc[b][n][v + 1], acc[b][n][v + 2], acc[b][n][v + 3]);
+          flush(a.out, a.ldo, r0, c0, a.R - r0, whole, four);
+        }
+      } else {
+        const int r0 = t.r0 + wr * PB * 32;
+#pragma unroll
+        for (int b = 0; b < PB; ++b)
+#pragma unroll
+          for (int v = 0; v < 16; v += 4)
+            put16(b * 32 + v * 2 + half * 4, acc[b][n][v], acc[b][n][v + 1], acc[b][n][v + 2], acc[b][n][v + 3]);
+        flush(a.out, a.ldo, r0, c0, a.R - r0, whole, two);
       }
     }
+    stores = GATED ? (a.gu != nullptr ? 6 : 2) * NQ : (a.out_dtype == MOE_DTYPE_FP32 ? 8 : 4) * NQ;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads write this block's LDS
 }
