@@ -36,49 +36,37 @@ __device__ __forceinline__ uint4 keep(uint4 v, bool in) {
 }
 
 // Tile number `tile` of TR sorted rows each, an adapter's tiles after the ones of the
-// adapters below: its adapter and rows. Every block counts the tiles of all adapters.
+// adapters below: its adapter and rows. Every wave counts the tiles of all adapters up to
+// it, 256 at a time.
 struct AdapterTile {
   int adapter, row0, rows;  // rows 0: no such tile
 };
 template <int TR>
 __device__ __forceinline__ AdapterTile find_tile(const AdapterArgs& a, int tile) {
-  constexpr int kPer = kMaxExperts / kThreads;
-  __shared__ int s_wave[kWaves];
-  __shared__ int s_tile[3];
-  const int tid = threadIdx.x, lane = lane_id(), wv = wave_index();
-  if (tid == 0) s_tile[2] = 0;
-  int lo[kPer], hi[kPer], sum = 0;
+  const int lane = lane_id();
+  int below = 0;  // tiles of the adapters looked at
+  for (int e0 = 0; e0 < a.A; e0 += 4 * kWave) {
+    int lo[4], hi[4];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * kThreads + tid;  // adapters below kThreads in one load
-    lo[i] = hi[i] = 0;
-    if (i * kThreads < a.A && e < a.A) {
-      lo[i] = min(max(a.offsets[e], 0), a.M);
-      hi[i] = min(a.offsets[e + 1], a.M);
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + i * kWave + lane;
+      lo[i] = a.offsets[min(e, a.A)];
+      hi[i] = a.offsets[min(e + 1, a.A)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int first = min(max(lo[i], 0), a.M), last = min(hi[i], a.M);
+      const int n = last > first ? (last - first + TR - 1) / TR : 0, at = below + wave_incl_scan(n) - n;
+      const uint64_t mine = ballot(tile >= at && tile < at + n);
+      if (mine != 0) {
+        const int l = __builtin_ctzll(mine);
+        const int row0 = __builtin_amdgcn_readlane(first + (tile - at) * TR, l);
+        return {e0 + i * kWave + l, row0, min(TR, __builtin_amdgcn_readlane(last, l) - row0)};
+      }
+      below = __builtin_amdgcn_readlane(at + n, kWave - 1);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (i * kThreads >= a.A) break;
-    const int n = hi[i] > lo[i] ? (hi[i] - lo[i] + TR - 1) / TR : 0;
-    const int incl = wave_incl_scan(n);
-    __syncthreads();
-    if (lane == kWave - 1) s_wave[wv] = incl;
-    __syncthreads();
-    int at = sum + incl - n;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wv) at += s_wave[w];
-      sum += s_wave[w];
-    }
-    if (tile >= at && tile < at + n) {
-      s_tile[0] = i * kThreads + tid;
-      s_tile[1] = lo[i] + (tile - at) * TR;
-      s_tile[2] = min(TR, hi[i] - s_tile[1]);
-    }
-  }
-  __syncthreads();
-  return {__builtin_amdgcn_readfirstlane(s_tile[0]), __builtin_amdgcn_readfirstlane(s_tile[1]),
-          __builtin_amdgcn_readfirstlane(s_tile[2])};
+  return {0, 0, 0};
 }
 
 // Row of x of a sorted row, or -1.
@@ -87,157 +75,205 @@ __device__ __forceinline__ int row_of(const AdapterArgs& a, int sorted) {
   return r >= 0 && r < a.M ? r : -1;
 }
 
-// t of a tile's rows over one part of K. RB: 16-row blocks of A. OWN: a wave has 16
-// rows of the tile (64 in all) and the whole part; else the waves split the part, and
-// join in LDS.
-template <int DT, int RB, bool OWN>
-__global__ __launch_bounds__(kThreads) void adapter_down_kernel(AdapterArgs a) {
-  constexpr int TR = OWN ? 64 : 16;
-  constexpr int U = RB >= 4 ? 2 : 4;  // K steps of 32 loaded together
-  const AdapterTile t = find_tile<TR>(a, blockIdx.x);
+// t of a tile's rows over one part of K, which the four waves split again and join in
+// LDS. RB, MT: 16-row blocks of A and of the tile.
+template <int DT, int RB, int MT>
+__global__ __launch_bounds__(kThreads, RB * MT >= 16 ? 2 : 4) void adapter_down_kernel(AdapterArgs a) {
+  constexpr int D = RB + MT <= 2 ? 4 : RB + MT <= 5 ? 2 : 1;  // steps of 64 of K in flight
+  const AdapterTile t = find_tile<16 * MT>(a, blockIdx.x);
   if (t.rows == 0) return;
   const int lane = lane_id(), wv = wave_index(), c = lane & 15, q = lane >> 4;
-  const int nk = (a.K + 31) >> 5, parts = a.splits * (OWN ? 1 : kWaves);
-  const int part = blockIdx.y * (OWN ? 1 : kWaves) + (OWN ? 0 : wv);
+  const int nk = (a.K + 63) >> 6, parts = a.splits * kWaves, part = blockIdx.y * kWaves + wv;
   const int k0 = static_cast<int>(static_cast<int64_t>(nk) * part / parts);
-  const int k1 = static_cast<int>(static_cast<int64_t>(nk) * (part + 1) / parts);
-  const int first = OWN ? wv * 16 : 0, rows = min(16, t.rows - first);
-  f32x4_t acc[RB];
+  const int nsteps = static_cast<int>(static_cast<int64_t>(nk) * (part + 1) / parts) - k0;
+  // lanes of rows that are not there read the tile's first: their columns of the result
+  // are not stored, and no column meets another
+  const uint16_t* x[MT];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  if (rows > 0) {
-    // lanes of rows that are not there read the tile's first: their columns of the
-    // result are not stored, and no column meets another (the same for rows of A)
-    const int row = max(row_of(a, t.row0 + first + (c < rows ? c : 0)), 0);
-    const uint16_t* const x = static_cast<const uint16_t*>(a.x) + row * a.ldx + q * 8;
-    const uint16_t* w[RB];
+  for (int m = 0; m < MT; ++m) {
+    const int r = m * 16 + c;
+    x[m] = static_cast<const uint16_t*>(a.x) + max(row_of(a, t.row0 + (r < t.rows ? r : 0)), 0) * a.ldx;
+  }
+  const __amdgpu_buffer_rsrc_t wb = make_rsrc(
+      static_cast<const uint16_t*>(a.a) + static_cast<int64_t>(t.adapter) * a.R * a.K, kNoRow);
+  uint32_t woff[RB];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-      w[b] = static_cast<const uint16_t*>(a.a) +
-             (static_cast<int64_t>(t.adapter) * a.R + min(b * 16 + c, a.R - 1)) * a.K + q * 8;
-    const int whole = min(k1, a.K >> 5);
-    int k = k0;
-    for (; k + U <= whole; k += U) {
-      uint4 xf[U], wf[U][RB];
+  for (int b = 0; b < RB; ++b) woff[b] = b * 16 + c < a.R ? (b * 16 + c) * static_cast<uint32_t>(a.K) * 2 : kNoRow;
+  f32x4_t acc[RB][MT];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        xf[u] = ld16(x + (k + u) * 32);
+  for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int b = 0; b < RB; ++b) wf[u][b] = ld16(w[b] + (k + u) * 32);
-      }
+    for (int m = 0; m < MT; ++m) acc[b][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint4 xf[D][MT][2], wf[D][RB][2];
+  auto load = [&](int d, int step) {  // both halves of a row's 128 bytes together
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+    for (int j = 0; j < 2; ++j) {
+      const int k = (k0 + min(step, nsteps - 1)) * 64 + j * 32 + q * 8;
+      const bool in = k < a.K;  // pieces past the end of K count as zeros on both sides
 #pragma unroll
-        for (int b = 0; b < RB; ++b) acc[b] = mfma16<DT>(wf[u][b], xf[u], acc[b]);
+      for (int m = 0; m < MT; ++m) xf[d][m][j] = ld16(x[m] + (in ? k : 0));
+#pragma unroll
+      for (int b = 0; b < RB; ++b) wf[d][b][j] = bld16(wb, in ? woff[b] + k * 2 : kNoRow);
     }
-    for (; k < k1; ++k) {  // the rest, and pieces of 8 past the end of K
-      const bool in = k * 32 + q * 8 < a.K;
-      const int at = in ? k * 32 : 0;
-      const uint4 xf = keep(ld16(in ? x + at : x - q * 8), in);
+  };
+  if (nsteps > 0) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b) acc[b] = mfma16<DT>(keep(ld16(in ? w[b] + at : w[b] - q * 8), in), xf, acc[b]);
+    for (int d = 0; d < D; ++d) load(d, d);
+    for (int s0 = 0; s0 < nsteps; s0 += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (s0 + d < nsteps) {
+          const int k = (k0 + s0 + d) * 64;
+          if (k + 64 > a.K) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int m = 0; m < MT; ++m) xf[d][m][j] = keep(xf[d][m][j], k + j * 32 + q * 8 < a.K);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+              for (int m = 0; m < MT; ++m) acc[b][m] = mfma16<DT>(wf[d][b][j], xf[d][m][j], acc[b][m]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (s0 + d + D < nsteps) load(d, s0 + d + D);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
-  // lane (c, q), register v of block b: t[row c, 16 b + 4 q + v]
-  float* const out = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + t.row0 + first) * a.R;
-  if constexpr (OWN) {
-    if (c < rows)
+  // lane (c, q), register v of block (b, m): t[row 16 m + c, 16 b + 4 q + v]
+  constexpr int kBlocks = RB * MT, kOnce = kBlocks < 8 ? kBlocks : 8;  // blocks joined at a time
+  __shared__ f32x4_t s_part[kWaves][kOnce][kWave];
+  float* const out = a.part + (static_cast<int64_t>(blockIdx.y) * a.M + t.row0) * a.R;
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-        if (b * 16 + q * 4 < a.R)
-          *reinterpret_cast<f32x4_t*>(out + static_cast<int64_t>(c) * a.R + b * 16 + q * 4) = acc[b];
-  } else {
-    __shared__ f32x4_t s_part[kWaves][RB][kWave];
+  for (int at = 0; at < kBlocks; at += kOnce) {
+    if (at > 0) __syncthreads();
 #pragma unroll
-    for (int b = 0; b < RB; ++b) s_part[wv][b][lane] = acc[b];
+    for (int i = 0; i < kOnce; ++i) s_part[wv][i][lane] = acc[(at + i) / MT][(at + i) % MT];
     __syncthreads();
-    for (int b = wv; b < RB; b += kWaves) {
-      f32x4_t v = s_part[0][b][lane];
+    for (int i = wv; i < kOnce; i += kWaves) {
+      f32x4_t v = s_part[0][i][lane];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += s_part[w][b][lane];
-      if (c < rows && b * 16 + q * 4 < a.R)
-        *reinterpret_cast<f32x4_t*>(out + static_cast<int64_t>(c) * a.R + b * 16 + q * 4) = v;
+      for (int w = 1; w < kWaves; ++w) v += s_part[w][i][lane];
+      const int r = (at + i) / MT * 16 + q * 4, m = (at + i) % MT * 16 + c;
+      if (m < t.rows && r < a.R) *reinterpret_cast<f32x4_t*>(out + static_cast<int64_t>(m) * a.R + r) = v;
     }
   }
 }
 
-// Sixteen elements of a row of base or out, as floats; n of them there.
+// A lane's 16-byte pieces of a row of base or out, of which n elements are there.
 template <int OT>
-__device__ __forceinline__ void load16(const void* p, int n, float (&f)[16]) {
-  constexpr int kVec = Row<OT>::kVec;
-  const uint8_t* const b = static_cast<const uint8_t*>(p);
-  if (n >= 16) {
+__device__ __forceinline__ uint4 load_piece(const void* p, int n) {
+  constexpr int kVec = Row<OT>::kVec, kSize = Row<OT>::kSize;
+  if (n >= kVec) return ld16_any<false>(p);
+  uint4 v = {0u, 0u, 0u, 0u};
+  float f[kVec];
 #pragma unroll
-    for (int i = 0; i < 16; i += kVec) Row<OT>::unpack(ld16_any<false>(b + i * Row<OT>::kSize), f + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = i < n ? Row<OT>::get(b + i * Row<OT>::kSize) : 0.0f;
-  }
+  for (int i = 0; i < kVec; ++i) f[i] = i < n ? Row<OT>::get(static_cast<const uint8_t*>(p) + i * kSize) : 0.0f;
+  v = Row<OT>::pack(f);
+  return v;
 }
 template <int OT>
-__device__ __forceinline__ void store16(void* p, int n, const float (&f)[16]) {
-  constexpr int kVec = Row<OT>::kVec;
-  uint8_t* const b = static_cast<uint8_t*>(p);
-  if (n >= 16) {
-#pragma unroll
-    for (int i = 0; i < 16; i += kVec) st16_any<false>(b + i * Row<OT>::kSize, Row<OT>::pack(f + i));
+__device__ __forceinline__ void store_piece(void* p, int n, const float* f) {
+  constexpr int kVec = Row<OT>::kVec, kSize = Row<OT>::kSize;
+  if (n >= kVec) {
+    st16_any<false>(p, Row<OT>::pack(f));
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) Row<OT>::put(b + i * Row<OT>::kSize, f[i]);
+    for (int i = 0; i < kVec; ++i)
+      if (i < n) Row<OT>::put(static_cast<uint8_t*>(p) + i * kSize, f[i]);
   }
 }
 
 // out of a tile's rows and a span of N. RS: 32-steps of R; MT: 16-row blocks of the
-// tile. t is summed over the parts of K and goes to LDS as two halves, t = hi + lo:
-// B is exact in its type, so the products keep t to 2^-16 (bf16) or 2^-22 (fp16)
-// at twice the MFMAs, which memory hides. In fp16 a row of t is first divided by a
-// power of two that brings its largest value below 2, past neither end of the range.
+// tile. t is summed over the parts of K and goes to LDS as a sum of terms in B's type:
+// hi + lo keep t to 2^-16 in bfloat16 (2^-22 in half), which is past a 16-bit result;
+// results in 32 bits from bfloat16 take a third term (2^-24). The MFMAs this costs hide
+// behind memory. In half a row of t is first divided by a power of two that brings its
+// largest value below 2, past neither end of the range.
 //
-// MFMA j of four on 64 columns takes column 16 (i / 4) + 4 j + i % 4 as its row i, so
-// a lane's four results of four MFMAs are sixteen neighbours of a row of out.
+// Of four MFMAs on 64 columns, number j takes column col(j, i / 4) + i % 4 as its row i: so
+// a lane's results are 16-byte pieces of a row of out, and the pieces of four lanes lie
+// side by side.
 template <int DT, int OT, int RS, int MT>
-__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int tiles, int span) {
+__global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int tiles, int span, int spans) {
   constexpr int TR = 16 * MT, kPad = 8, kRow = RS * 32 + kPad;  // halves of a row of t in LDS
-  constexpr int OS = Row<OT>::kSize;
+  constexpr int kTerms = DT == MOE_DTYPE_BF16 && OT == MOE_DTYPE_FP32 ? 3 : 2;
+  constexpr int OS = Row<OT>::kSize, kVec = Row<OT>::kVec, kPieces = 16 / kVec;
+  constexpr auto col = [](int j, int q) { return OS == 4 ? j * 16 + q * 4 : (j >> 1) * 32 + q * 8 + (j & 1) * 4; };
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_index(), c = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.y * span, n1 = min(a.N, n0 + span);
+  // spans of the same rows are neighbours
+  const int tile = blockIdx.x / spans, n0 = (blockIdx.x - tile * spans) * span, n1 = min(a.N, n0 + span);
   uint8_t* const out = static_cast<uint8_t*>(a.out);
   const uint8_t* const base = static_cast<const uint8_t*>(a.base);
-  if (static_cast<int>(blockIdx.x) >= tiles) {
+  if (tile >= tiles) {
     // rows without an adapter, where out is an array of its own
-    const int r0 = (blockIdx.x - tiles) * TR;
+    const int r0 = (tile - tiles) * TR;
     for (int r = r0 + wv; r < min(a.M, r0 + TR); r += kWaves) {
       if (a.slot_row[r] >= 0) continue;
-      for (int n = n0 + lane * 16; n < n1; n += kWave * 16) {
-        float f[16] = {};
-        const int left = min(16, n1 - n);
-        if (base != nullptr) load16<OT>(base + (r * a.ldb + n) * OS, left, f);
-        store16<OT>(out + (r * a.ldo + n) * OS, left, f);
+      for (int n = n0 + lane * kVec; n < n1; n += kWave * kVec) {
+        float f[kVec] = {};
+        if (base != nullptr) Row<OT>::unpack(load_piece<OT>(base + (r * a.ldb + n) * OS, n1 - n), f);
+        store_piece<OT>(out + (r * a.ldo + n) * OS, n1 - n, f);
       }
     }
     return;
   }
-  __shared__ __attribute__((aligned(16))) uint16_t s_hi[TR * kRow], s_lo[TR * kRow];
+  __shared__ __attribute__((aligned(16))) uint16_t s_t[kTerms][TR * kRow];
   __shared__ float s_scale[TR];
-  __shared__ int s_row[TR];
-  const AdapterTile t = find_tile<TR>(a, blockIdx.x);
+  const AdapterTile t = find_tile<TR>(a, tile);
   if (t.rows == 0) return;
-  // t: sixteen threads a row, 8 RS / 4 values each
-  constexpr int kPer = RS * 2;
-  for (int m = tid >> 4; m < TR; m += kThreads / 16) {
-    const int r = (tid & 15) * kPer;
-    float v[kPer];
+  // The loads that need no t go out first.
+  int row[MT];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
-    if (m < t.rows) {
-      const float* p = a.part + static_cast<int64_t>(t.row0 + m) * a.R + r;
-      for (int s = 0; s < a.splits; ++s, p += static_cast<int64_t>(a.M) * a.R)
+  for (int m = 0; m < MT; ++m) row[m] = m * 16 + c < t.rows ? row_of(a, t.row0 + m * 16 + c) : -1;
+  const uint16_t* const b = static_cast<const uint16_t*>(a.b) + static_cast<int64_t>(t.adapter) * a.N * a.R;
+  uint4 w[4][RS], old[MT][kPieces];
+  auto load = [&](int n) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (r + i < a.R) v[i] += p[i];
+    for (int j = 0; j < 4; ++j) {
+      const int at = min(n + col(j, c >> 2) + (c & 3), a.N - 1);
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        const int r = s * 32 + q * 8;
+        w[j][s] = ld16(b + static_cast<int64_t>(at) * a.R + (r < a.R ? r : 0));
+      }
     }
-    float f = a.scale != nullptr ? a.scale[t.adapter] : 1.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = n + col(i * kVec / 4, q);
+        old[m][i] = uint4{0u, 0u, 0u, 0u};
+        if (base != nullptr && row[m] >= 0 && at < n1) old[m][i] = load_piece<OT>(base + (row[m] * a.ldb + at) * OS, n1 - at);
+      }
+  };
+  int n = n0 + wv * 64;
+  if (n < n1) load(n);
+  // t: sixteen threads a row, 2 RS values each
+  constexpr int kPer = RS * 2, kOnce = 4;
+  typedef float vec_t __attribute__((ext_vector_type(kPer), aligned(8)));
+  const float factor = a.scale != nullptr ? a.scale[t.adapter] : 1.0f;
+#pragma unroll
+  for (int m0 = 0; m0 < TR; m0 += kThreads / 16) {
+    const int m = m0 + (tid >> 4), r = (tid & 15) * kPer;
+    // R is a multiple of 8: a thread's values are all there or none is
+    const bool in = m < t.rows && r < a.R;
+    const float* p = a.part + static_cast<int64_t>(t.row0 + (in ? m : 0)) * a.R + (in ? r : 0);
+    const int64_t step = static_cast<int64_t>(a.M) * a.R;
+    vec_t v = {};
+    for (int s = 0; s < a.splits; s += kOnce) {
+      vec_t u[kOnce];
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) u[i] = *reinterpret_cast<const vec_t*>(p + min(s + i, a.splits - 1) * step);
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i)
+        if (s + i < a.splits) v += u[i];
+    }
+    if (!in) v = vec_t{};
+    float f = factor;
     if constexpr (DT == MOE_DTYPE_FP16) {
       float most = 0.0f;
 #pragma unroll
@@ -252,69 +288,57 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      float hi;
-      if constexpr (DT == MOE_DTYPE_BF16) {
-        const uint16_t h = f32_to_bf16(v[i]);
-        hi = bf16_to_f32(h);
-        s_hi[m * kRow + r + i] = h;
-      } else {
-        const _Float16 h = static_cast<_Float16>(v[i]);
-        hi = static_cast<float>(h);
-        s_hi[m * kRow + r + i] = __builtin_bit_cast(uint16_t, h);
+      float left = v[i];
+#pragma unroll
+      for (int k = 0; k < kTerms; ++k) {
+        uint16_t h;
+        Row<DT>::put(&h, left);
+        s_t[k][m * kRow + r + i] = h;
+        const float term = Row<DT>::get(&h);
+        left = fabsf(term) < __builtin_inff() ? left - term : 0.0f;  // nothing beside an infinity or NaN
       }
-      const float lo = fabsf(hi) < __builtin_inff() ? v[i] - hi : 0.0f;  // nothing beside an infinity or NaN
-      if constexpr (DT == MOE_DTYPE_BF16) s_lo[m * kRow + r + i] = f32_to_bf16(lo);
-      else s_lo[m * kRow + r + i] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(lo));
     }
-    if ((tid & 15) == 0) {
-      s_scale[m] = f;
-      s_row[m] = m < t.rows ? row_of(a, t.row0 + m) : -1;
-    }
+    if ((tid & 15) == 0) s_scale[m] = f;
   }
   __syncthreads();
-  int row[MT];
   float scale[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    row[m] = s_row[m * 16 + c];
-    scale[m] = s_scale[m * 16 + c];
-  }
-  const uint16_t* const b = static_cast<const uint16_t*>(a.b) + static_cast<int64_t>(t.adapter) * a.N * a.R;
-  for (int n = n0 + wv * 64; n < n1; n += kWaves * 64) {
-    uint4 w[4][RS];
+  for (int m = 0; m < MT; ++m) scale[m] = s_scale[m * 16 + c];
+  for (; n < n1; n += kWaves * 64) {
+    if (a.R % 32 != 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = min(n + 16 * (c >> 2) + 4 * j + (c & 3), a.N - 1);
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int s = 0; s < RS; ++s) {
-        const int r = s * 32 + q * 8;
-        w[j][s] = keep(ld16(b + static_cast<int64_t>(at) * a.R + (r < a.R ? r : 0)), r < a.R);
-      }
+        for (int s = 0; s < RS; ++s) w[j][s] = keep(w[j][s], s * 32 + q * 8 < a.R);
     }
-    const int col = n + q * 16, left = min(16, n1 - col);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m * 16 >= t.rows) break;
-      float f[16] = {};
-      const bool in = row[m] >= 0 && left > 0;
-      if (in && base != nullptr) load16<OT>(base + (row[m] * a.ldb + col) * OS, left, f);
       f32x4_t acc[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        const int at = (m * 16 + c) * kRow + s * 32 + q * 8;
-        const uint4 hi = *reinterpret_cast<const uint4*>(s_hi + at), lo = *reinterpret_cast<const uint4*>(s_lo + at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mfma16<DT>(w[j][s], hi, mfma16<DT>(w[j][s], lo, acc[j]));
+        for (int k = kTerms - 1; k >= 0; --k) {
+          const uint4 term = *reinterpret_cast<const uint4*>(&s_t[k][(m * 16 + c) * kRow + s * 32 + q * 8]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma16<DT>(w[j][s], term, acc[j]);
+        }
       }
-      if (!in) continue;
+      if (row[m] < 0) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = n + col(i * kVec / 4, q);
+        if (at >= n1) continue;
+        float f[kVec];
+        Row<OT>::unpack(old[m][i], f);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) f[4 * j + v] += scale[m] * acc[j][v];
-      store16<OT>(out + (row[m] * a.ldo + col) * OS, left, f);
+        for (int v = 0; v < kVec; ++v) f[v] += scale[m] * acc[i * kVec / 4 + v / 4][v % 4];
+        store_piece<OT>(out + (row[m] * a.ldo + at) * OS, n1 - at, f);
+      }
     }
+    if (n + kWaves * 64 < n1) load(n + kWaves * 64);
   }
 }
 
@@ -330,9 +354,9 @@ template <int DT, int RB>
 void down(const AdapterArgs& a, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(tile_bound(a)), static_cast<unsigned>(a.splits));
   if (many_rows(a.M, a.A))
-    hipLaunchKernelGGL((adapter_down_kernel<DT, RB, true>), grid, dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((adapter_down_kernel<DT, RB, 4>), grid, dim3(kThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((adapter_down_kernel<DT, RB, false>), grid, dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((adapter_down_kernel<DT, RB, 1>), grid, dim3(kThreads), 0, st, a);
 }
 
 template <int DT, int OT, int RS>
@@ -344,14 +368,15 @@ void up(const AdapterArgs& a, hipStream_t st) {
   const int64_t others = a.out == a.base ? 0 : (a.M + tr - 1) / tr;
   const int64_t n64 = (a.N + 63) / 64;
   // spans of N: enough blocks for the card, each with at least one piece a wave
-  const int64_t want = std::max<int64_t>(1, 2048 / std::max<int64_t>(tiles, 1));
+  const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(tiles, 1));
   const int64_t per = std::max<int64_t>(kWaves, (n64 + want - 1) / want);
   const int span = static_cast<int>((per + kWaves - 1) / kWaves * kWaves * 64);
-  const dim3 grid(static_cast<unsigned>(tiles + others), static_cast<unsigned>((a.N + span - 1) / span));
+  const int spans = (a.N + span - 1) / span;
+  const dim3 grid(static_cast<unsigned>((tiles + others) * spans));
   if (many)
-    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 4>), grid, dim3(kThreads), 0, st, a, static_cast<int>(tiles), span);
+    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 4>), grid, dim3(kThreads), 0, st, a, static_cast<int>(tiles), span, spans);
   else
-    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 1>), grid, dim3(kThreads), 0, st, a, static_cast<int>(tiles), span);
+    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 1>), grid, dim3(kThreads), 0, st, a, static_cast<int>(tiles), span, spans);
 }
 
 template <int DT, int OT>
@@ -374,11 +399,9 @@ void both(const AdapterArgs& a, hipStream_t st) {
 }  // namespace
 
 int adapter_splits(int64_t M, int64_t A, int64_t K) {
-  const bool many = many_rows(M, A);
-  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(M, M / (many ? 64 : 16) + std::min(A, M)));
-  const int64_t steps = (K + 31) / 32 / (many ? 1 : kWaves);  // a wave's, unsplit
-  const int64_t by_card = (many ? 1024 : 512) / tiles, by_steps = steps / 4;
-  return static_cast<int>(std::clamp<int64_t>(std::min(by_card, by_steps), 1, 16));
+  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(M, M / (many_rows(M, A) ? 64 : 16) + std::min(A, M)));
+  const int64_t steps = (K + 63) / 64 / kWaves;  // a wave's, unsplit
+  return static_cast<int>(std::clamp<int64_t>(std::min(512 / tiles, steps / 2), 1, 16));
 }
 
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t st) {
