@@ -173,6 +173,7 @@ hipError_t launch_tile_forward(const TileArgs& a, bool gated, hipStream_t st);
 hipError_t launch_few_rows(const TileArgs& a, bool gated, hipStream_t st);  // forward (few_rows.hip)
 hipError_t launch_tile_row_grad(const TileArgs& a, hipStream_t st);
 hipError_t launch_tile_mat_grad(const TileArgs& a, hipStream_t st);
+hipError_t launch_tile_gradients(const TileArgs& mat, const TileArgs& row, hipStream_t st);
 
 // Gradient of the activation: dgu [M, 2 I] from dh [M, I] and the pre-activations.
 struct ActGradArgs {

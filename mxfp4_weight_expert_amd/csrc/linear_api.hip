@@ -133,31 +133,26 @@ int check_backward(const Product& p, const int32_t* offsets) {
 // dx and dw from the gradient of the product, either of them null.
 int gradients(const Product& p, const void* dout, const void* x, const int32_t* offsets, const void* w, void* dx,
               void* dw, hipStream_t st) {
-  if (dx != nullptr && p.M > 0) {
-    TileArgs a = tile_args(p, offsets);
-    a.p = w;
-    a.q = dout;
-    a.out = dx;
-    a.R = static_cast<int>(p.K);
-    a.I = static_cast<int>(p.N);
-    a.ldp = a.ldo = p.K;
-    a.ldq = p.N;
-    const int rc = status(launch_tile_row_grad(a, st));
-    if (rc != MOE_OK) return rc;
-  }
-  if (dw != nullptr) {
-    TileArgs a = tile_args(p, offsets);
-    a.p = x;
-    a.q = dout;
-    a.out = dw;
-    a.R = static_cast<int>(p.K);
-    a.C = static_cast<int>(p.N);
-    a.ldp = a.ldo = p.K;
-    a.ldq = p.N;
-    a.out_dtype = p.out_dtype;
-    return status(launch_tile_mat_grad(a, st));
-  }
-  return MOE_OK;
+  TileArgs row = tile_args(p, offsets), mat = row;
+  row.p = w;
+  row.q = dout;
+  row.out = dx;
+  row.R = static_cast<int>(p.K);
+  row.I = static_cast<int>(p.N);
+  row.ldp = row.ldo = p.K;
+  row.ldq = p.N;
+  mat.p = x;
+  mat.q = dout;
+  mat.out = dw;
+  mat.R = static_cast<int>(p.K);
+  mat.C = static_cast<int>(p.N);
+  mat.ldp = mat.ldo = p.K;
+  mat.ldq = p.N;
+  mat.out_dtype = p.out_dtype;
+  const bool rows = dx != nullptr && p.M > 0;
+  if (rows && dw != nullptr) return status(launch_tile_gradients(mat, row, st));
+  if (rows) return status(launch_tile_row_grad(row, st));
+  return dw != nullptr ? status(launch_tile_mat_grad(mat, st)) : MOE_OK;
 }
 
 int check(const moe_adapter_shape* s) {

@@ -10,8 +10,8 @@ hipError_t launch_tile_forward(const TileArgs& a, bool gated, hipStream_t st) {
   // rows 17 and 26, 32 rows 29 and 30).
   if (a.offsets == nullptr ? a.M <= 16 : a.M <= int64_t{8} * a.E) return launch_few_rows(a, gated, st);
   if (a.dtype == MOE_DTYPE_BF16)
-    return gated ? tile_size<kForward, true, MOE_DTYPE_BF16>(a, st) : tile_size<kForward, false, MOE_DTYPE_BF16>(a, st);
-  return gated ? tile_size<kForward, true, MOE_DTYPE_FP16>(a, st) : tile_size<kForward, false, MOE_DTYPE_FP16>(a, st);
+    return gated ? tile_run<kForward, true, MOE_DTYPE_BF16>(a, st) : tile_run<kForward, false, MOE_DTYPE_BF16>(a, st);
+  return gated ? tile_run<kForward, true, MOE_DTYPE_FP16>(a, st) : tile_run<kForward, false, MOE_DTYPE_FP16>(a, st);
 }
 
 }  // namespace moe

@@ -31,15 +31,36 @@ template <int T>
 int64_t tile_blocks() {
   return std::max(gpu_cus() / 8 * 8, 8) * (T == 128 ? 2 : 1);
 }
-template <int T, int MODE, bool GATED, int DT>
-hipError_t tile_go(const TileArgs& a, hipStream_t st) {
+template <int T, int MODE, bool GATED>
+int64_t tile_items(const TileArgs& a) {
   const int64_t wide = GATED ? T / 2 : T, nr = (a.R + wide - 1) / wide;
-  const int64_t items = nr * (MODE == kMatGrad ? static_cast<int64_t>(a.E) * ((a.C + T - 1) / T)
-                                               : (a.M + T - 1) / T + (a.offsets != nullptr ? std::min(a.E, a.M) : 0));
-  const int64_t blocks = std::min((items + 7) / 8 * 8, tile_blocks<T>());
-  const int lds = tile_lds(T) + (MODE != kMatGrad && a.offsets != nullptr ? (a.E + 1) * 4 : 0);
-  hipLaunchKernelGGL((tile_product_kernel<T, MODE, GATED, DT>), dim3(static_cast<unsigned>(blocks)),
+  return nr * (MODE == kMatGrad ? static_cast<int64_t>(a.E) * ((a.C + T - 1) / T)
+                                : (a.M + T - 1) / T + (a.offsets != nullptr ? std::min(a.E, a.M) : 0));
+}
+template <int T, int STEP>
+int tile_room(const TileArgs& a) {  // LDS: stages, and the experts' first tiles
+  return tile_lds(T, STEP) + (a.offsets != nullptr ? (a.E + 1) * 4 : 0);
+}
+template <int T, int STEP, int MODE, bool GATED, int DT>
+hipError_t tile_go(const TileArgs& a, hipStream_t st) {
+  const int64_t blocks = std::min((tile_items<T, MODE, GATED>(a) + 7) / 8 * 8, tile_blocks<T>());
+  const int lds = tile_room<T, STEP>(a);
+  hipLaunchKernelGGL((tile_product_kernel<T, STEP, MODE, GATED, DT>), dim3(static_cast<unsigned>(blocks)),
                      dim3(tile_threads(T)), lds, st, a);
+  return hipGetLastError();
+}
+// How many tiles of the rows' gradient take as long as one of the matrices'.
+inline double tile_ratio(const TileArgs& mat, const TileArgs& row) {
+  return static_cast<double>(mat.M) / mat.E / row.I;
+}
+template <int T, int STEP, int DT>
+hipError_t tile_gradients_go(const TileArgs& mat, const TileArgs& row, hipStream_t st) {
+  const int64_t first = tile_items<T, kMatGrad, false>(mat), all = first + tile_items<T, kRowGrad, false>(row);
+  const int64_t blocks = std::min((all + 7) / 8 * 8, tile_blocks<T>());
+  const TileShare share = {static_cast<int>(first), static_cast<int>(std::clamp(tile_ratio(mat, row) + 0.5, 0.0, 1024.0))};
+  const int lds = tile_room<T, STEP>(mat);
+  hipLaunchKernelGGL((tile_gradients_kernel<T, STEP, DT>), dim3(static_cast<unsigned>(blocks)), dim3(tile_threads(T)),
+                     lds, st, mat, row, share);
   return hipGetLastError();
 }
 
@@ -55,19 +76,40 @@ double tile_time(const TileArgs& a) {
   const int64_t wide = GATED ? T / 2 : T, nr = (a.R + wide - 1) / wide;
   const double across = MODE == kMatGrad ? a.C : rows;
   const double tiles = std::ceil(across / T) * nr * (MODE == kMatGrad ? a.E : std::min<double>(a.E, a.M));
-  const double steps = std::ceil((MODE == kMatGrad ? rows : a.I) / kStep), fill = std::min(1.0, across / T);
+  const double steps = std::ceil((MODE == kMatGrad ? rows : a.I) / 32), fill = std::min(1.0, across / T);
   const double rounds = std::ceil(tiles / static_cast<double>(tile_blocks<T>()));
   if (T == 64) return rounds * (2.2 + steps * (tiles <= 128 ? 0.12 : 0.2));
   if (T == 256) return rounds * (7 + steps * (0.45 + 0.4 * fill));
   return tiles <= gpu_cus() ? 2.5 + steps * 0.27 : rounds * (5 + steps * (0.5 + 0.2 * fill));
 }
 
-template <int MODE, bool GATED, int DT>
-hipError_t tile_size(const TileArgs& a, hipStream_t st) {
+// Whether tiles of 256 take stages of 64 (tile_stage): where many rows make the matrix
+// cores and not memory the bound. 64 of 256 experts' 8192 x 8 rows forward 1338 us so, 1437
+// with stages of 32; half of 896 experts, 146 rows by this count, rows' gradient 27 us more.
+template <int MODE>
+bool long_stages(const TileArgs& a) {
+  return a.M >= (MODE == kMatGrad ? 2048 : 192) * static_cast<int64_t>(a.E);
+}
+
+// The kernel of a shape: tiles of 64, 128 or 256, these with stages of 32 or 64.
+enum TileKind { kTile64, kTile128, kTile256, kTile256Long };
+template <int MODE, bool GATED>
+TileKind tile_kind(const TileArgs& a) {
   const double t64 = tile_time<64, MODE, GATED>(a), t128 = tile_time<128, MODE, GATED>(a);
   const double t256 = tile_time<256, MODE, GATED>(a);
-  if (t64 <= std::min(t128, t256)) return tile_go<64, MODE, GATED, DT>(a, st);
-  return t128 <= t256 ? tile_go<128, MODE, GATED, DT>(a, st) : tile_go<256, MODE, GATED, DT>(a, st);
+  if (t64 <= std::min(t128, t256)) return kTile64;
+  if (t128 <= t256) return kTile128;
+  return long_stages<MODE>(a) ? kTile256Long : kTile256;
+}
+
+template <int MODE, bool GATED, int DT>
+hipError_t tile_run(const TileArgs& a, hipStream_t st) {
+  switch (tile_kind<MODE, GATED>(a)) {
+    case kTile64: return tile_go<64, 32, MODE, GATED, DT>(a, st);
+    case kTile128: return tile_go<128, 32, MODE, GATED, DT>(a, st);
+    case kTile256: return tile_go<256, 32, MODE, GATED, DT>(a, st);
+    default: return tile_go<256, 64, MODE, GATED, DT>(a, st);
+  }
 }
 
 }  // namespace moe

@@ -35,16 +35,20 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 enum { kForward, kRowGrad, kMatGrad };
 
-constexpr int kStep = 32;      // i of a stage
-constexpr int kSlots = 4;      // stages in LDS: one read, up to three in flight
 constexpr int PB = 2;          // 32-blocks of r of a wave
 // Tiles of T x T. T = 256, 128: T / 32 waves, each with 64 r and every second 32 c, share
 // the stages. T = 64: four waves take every fourth stage each, with stages of their own
 // and no barrier between them, and join their sums at the end.
 constexpr int tile_split(int T) { return T == 64 ? 4 : 1; }
 constexpr int tile_threads(int T) { return T == 64 ? 256 : T * 2; }
-constexpr int tile_stage(int T) { return 2 * T * kStep * 2; }  // bytes of both operands
-constexpr int tile_lds(int T) { return kSlots * tile_stage(T) * tile_split(T); }
+// Stages of STEP i: both operands' bytes of one, and how many are in LDS, one read and the
+// others in flight. Of 32 there are four, of 64 (tiles of 256 alone) two, with half the
+// barriers and whole 128-byte lines: 8192 x 8192 x 8192 878 us (forward), 843 and 893
+// (gradients) against 921, 903 and 915; but where memory bounds the tile the fewer bytes
+// in flight cost more (64 experts of 32 rows, K 7168 x 2 N 4096 765 us, 725).
+constexpr int tile_stage(int T, int STEP) { return 2 * T * STEP * 2; }
+constexpr int tile_slots(int STEP) { return STEP == 64 ? 2 : 4; }
+constexpr int tile_lds(int T, int STEP) { return tile_slots(STEP) * tile_stage(T, STEP) * tile_split(T); }
 
 template <int DT>
 __device__ __forceinline__ f32x16_t mfma32(uint4 a, uint4 b, f32x16_t c) {
@@ -69,11 +73,12 @@ __device__ __forceinline__ void load_to_lds(uint64_t base, uint32_t off, uint32_
                : "memory");  // compiled code sets m0 right before each of its own uses
 }
 
-// Rows of 64 bytes: 16-byte chunk c of row r lies at chunk c ^ chunk_swz(r). LDS serves
-// a 16-byte read sixteen lanes at a time, in groups of four neighbours: 0, 12, 20 and 24
-// on, then 4, 8, 16 and 28 on; the four chunks of these rows are different ones (no
-// conflicts; counted).
-__device__ __forceinline__ uint32_t chunk_swz(uint32_t r) { return r >> 2 & 3; }
+// Rows of STEP i (64 or 128 bytes): 16-byte chunk c of row r lies at chunk c ^
+// chunk_swz(r). LDS serves a 16-byte read sixteen lanes at a time, in groups of four
+// neighbours: 0, 12, 20 and 24 on, then 4, 8, 16 and 28 on; the chunks of these rows fall
+// on different banks (no conflicts; counted).
+template <int STEP>
+__device__ __forceinline__ uint32_t chunk_swz(uint32_t r) { return STEP == 32 ? r >> 2 & 3 : r >> 1 & 7; }
 // Rows of 512, 256 or 128 bytes: 64-byte piece g of row r lies at piece g ^ piece_swz(r): the
 // four rows of a transposing read, and those of its other half eight further on, fall on
 // different banks.
@@ -102,20 +107,28 @@ struct TileItem {
   int len;    // i to sum over
 };
 
-template <int T, int MODE, bool GATED, int DT>
-__global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product_kernel(TileArgs a) {
+// How a second list of tiles follows a first in one launch: blocks with one tile fewer of
+// the first take `more` of the second before the others take any.
+struct TileShare {
+  int items;  // of the first list; 0: none
+  int more;
+};
+
+template <int T, int kStep, int MODE, bool GATED, int DT>
+__device__ __forceinline__ void tile_product(const TileArgs& a, const TileShare first_list) {
   static_assert(!GATED || MODE == kForward, "the activation follows the forward product");
   constexpr bool kPInner = MODE == kForward;   // i is P's inner index
   constexpr bool kQInner = MODE != kMatGrad;
   constexpr int kWide = GATED ? T / 2 : T;      // r of a tile
   constexpr int KW = tile_split(T), WC = KW > 1 ? 1 : 2;  // waves along i, along c
   constexpr int NQ = T / (32 * WC);               // 32-blocks of c of a wave: every WC-th
-  constexpr int kThreads = tile_threads(T), kWaves = kThreads / 64, kStage = tile_stage(T), kSide = kStage / 2;
+  constexpr int kSlots = tile_slots(kStep), kHalves = kStep / 16;  // 16 i an MFMA
+  constexpr int kThreads = tile_threads(T), kWaves = kThreads / 64, kStage = tile_stage(T, kStep), kSide = kStage / 2;
   constexpr int kLoads = kSide / 1024 / (KW > 1 ? 1 : kWaves);  // a wave's loads of 1 KB of an operand's stage
   constexpr int kRow = 2 * T;                     // bytes of a row whose inner index is not i
   extern __shared__ __attribute__((aligned(1024))) uint8_t s_dyn[];
   __shared__ int32_t s_wave[kWaves];
-  int32_t* const s_first = reinterpret_cast<int32_t*>(s_dyn + tile_lds(T));  // grouped: tiles before each expert
+  int32_t* const s_first = reinterpret_cast<int32_t*>(s_dyn + tile_lds(T, kStep));  // grouped: tiles before each expert
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) uint8_t*)s_dyn));
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_index();
@@ -170,12 +183,20 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
   // each XCD has a range of its own, so that it meets them in the next round too. Experts,
   // whose tiles cost differently: the XCDs take turns (64 experts of 256 rows 1382 us,
   // 1512 with ranges; one matrix the other way 950 and 912).
-  const int walkers = static_cast<int>(gridDim.x) >> 3, xcd = blockIdx.x & 7, walker = blockIdx.x >> 3;
-  const int per = (items + 7) >> 3;
+  const int walkers = static_cast<int>(gridDim.x) >> 3, xcd = blockIdx.x & 7;
+  const bool ranges = a.offsets == nullptr;
+  const int width = ranges ? walkers : static_cast<int>(gridDim.x);  // blocks that share a run of items
+  const int place = ranges ? blockIdx.x >> 3 : xcd * walkers + (blockIdx.x >> 3);
+  const int per = ranges ? (items + 7) >> 3 : items, base = ranges ? xcd * per : 0;
+  const int busy = first_list.items == 0 ? 0 : (ranges ? (first_list.items + 7) >> 3 : first_list.items) % width;
+  const int idle = busy > 0 ? width - busy : 0, more = idle > 0 ? min(first_list.more, per / idle) : 0;
   auto item_of = [&](int k) {
-    const int at = k * walkers + walker;
-    if (a.offsets == nullptr) return at < per ? xcd * per + at : items;
-    return k * static_cast<int>(gridDim.x) + xcd * walkers + walker;
+    int at = k * width + place;
+    if (more > 0) {
+      if (place < busy) at = idle * more + k * width + idle + place;
+      else at = k < more ? k * idle + place - busy : idle * more + (k - more) * width + place - busy;
+    }
+    return at < per ? base + at : items;
   };
 
   auto decode = [&](int item) {
@@ -249,7 +270,8 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
       const uint32_t row = (lw * kLoads + j) * (1024 / kRow) + lane / (kRow / 16);
       const uint32_t across = ((lane / 4 % (kRow / 64)) ^ piece_swz<T>(row)) * 4 + (lane & 3);  // 16-byte chunk
       if constexpr (kPInner) {
-        const uint32_t rho = (lw * kLoads + j) * 16 + (lane >> 2), chunk = (lane & 3) ^ chunk_swz(rho);
+        const uint32_t rho = (lw * kLoads + j) * (512 / kStep) + lane / (kStep / 8);
+        const uint32_t chunk = (lane % (kStep / 8)) ^ chunk_swz<kStep>(rho);
         const uint32_t r = GATED ? gated_feature(rho) : rho;
         const bool in = t.r0 + r < static_cast<uint32_t>(a.R);
         poff[j] = in ? (r + (GATED && gated_up(rho) ? a.R : 0)) * static_cast<uint32_t>(a.ldp) * 2 + chunk * 16 : kNoRow;
@@ -260,7 +282,8 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
         pi[j] = row;
       }
       if constexpr (kQInner) {
-        const uint32_t c = (lw * kLoads + j) * 16 + (lane >> 2), chunk = (lane & 3) ^ chunk_swz(c);
+        const uint32_t c = (lw * kLoads + j) * (512 / kStep) + lane / (kStep / 8);
+        const uint32_t chunk = (lane % (kStep / 8)) ^ chunk_swz<kStep>(c);
         qoff[j] = c < static_cast<uint32_t>(t.cols) ? c * static_cast<uint32_t>(a.ldq) * 2 + chunk * 16 : kNoRow;
         qi[j] = chunk * 8;
       } else {
@@ -294,10 +317,11 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
 
   // ---- operands from LDS
   const int l32 = lane & 31, half = lane >> 5;
-  uint32_t pat[kPInner ? 2 : PB], qat[kQInner ? 2 : NQ];
+  uint32_t pat[kPInner ? kHalves : PB], qat[kQInner ? kHalves : NQ];
   if constexpr (kPInner) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) pat[s] = (wr * PB * 32 + l32) * 64 + (((2 * s + half) ^ chunk_swz(l32)) << 4);
+    for (int s = 0; s < kHalves; ++s)
+      pat[s] = (wr * PB * 32 + l32) * 2 * kStep + (((2 * s + half) ^ chunk_swz<kStep>(l32)) << 4);
   } else {
     const uint32_t row = half * 8 + (lane >> 2 & 3), gg = lane >> 4 & 1, q = lane & 3;
 #pragma unroll
@@ -305,7 +329,8 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
   }
   if constexpr (kQInner) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) qat[s] = kSide + (wc * 32 + l32) * 64 + (((2 * s + half) ^ chunk_swz(l32)) << 4);
+    for (int s = 0; s < kHalves; ++s)
+      qat[s] = kSide + (wc * 32 + l32) * 2 * kStep + (((2 * s + half) ^ chunk_swz<kStep>(l32)) << 4);
   } else {
     const uint32_t row = half * 8 + (lane >> 2 & 3), gg = lane >> 4 & 1, q = lane & 3;
 #pragma unroll
@@ -319,16 +344,16 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
     return uint4{u.x, u.y, v.x, v.y};
   };
   auto read_p = [&](const uint8_t* stage, int s, int b) {
-    if constexpr (kPInner) return ld16(stage + pat[s] + b * 32 * 64);
+    if constexpr (kPInner) return ld16(stage + pat[s] + b * 32 * 2 * kStep);
     else return transposed(stage + pat[b] + s * 16 * kRow);
   };
   auto read_q = [&](const uint8_t* stage, int s, int n) {
-    if constexpr (kQInner) return ld16(stage + qat[s] + n * WC * 32 * 64);
+    if constexpr (kQInner) return ld16(stage + qat[s] + n * WC * 32 * 2 * kStep);
     else return transposed(stage + qat[n] + s * 16 * kRow);
   };
 
-  // Waits until a stage's loads are done: those of the next two stages, and `stores`
-  // stores behind them, may be under way.
+  // Waits until a stage's loads are done: those of the stages after it, and
+  // `stores` stores behind them, may be under way.
   auto wait_stage = [&](int stores) {
     constexpr int kAhead = (kSlots - 2) * 2 * kLoads;
     if (stores >= 32) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead + 32) : "memory");
@@ -352,12 +377,12 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[b][n][v] = 0.0f;
 
-    // A stage's second half is multiplied after the next stage's barrier, while
+    // A stage's last 16 i are multiplied after the next stage's barrier, while
     // that stage's first operands are read.
     auto walk = [&](auto nqc) {
       constexpr int N = decltype(nqc)::value;
-      // Half a stage's products from operands in registers, with the LDS reads of the
-      // other half, written before them, between the first.
+      // Products of 16 i from operands in registers, with the LDS reads of the next 16,
+      // written before them, between the first.
       auto mul = [&](const uint4 (&p)[PB], const uint4 (&q)[NQ]) {
         constexpr int kMuls = PB * N, kReads = (kPInner ? PB : 2 * PB) + (kQInner ? N : 2 * N);
 #pragma unroll
@@ -375,9 +400,9 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
 #pragma unroll
       for (int n = 0; n < N; ++n) q1[n] = uint4{0, 0, 0, 0};
       for (int k = 0; k < stages; ++k) {
-        // this stage has come (three are in flight), and no wave still reads the slot
+        // this stage has come, and no wave still reads the slot
         // that the next loads go to
-        // (the stores of the last item's results, younger than three stages' loads, go on)
+        // (the stores of the last item's results, younger than its loads, go on)
         if (k >= kSlots - 1) stores = 0;
         wait_stage(stores);
         if constexpr (KW == 1) __builtin_amdgcn_s_barrier();
@@ -386,15 +411,18 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
         const uint8_t* const stage = ring + slot * kStage;
         if constexpr (N > 0) {
 #pragma unroll
-          for (int b = 0; b < PB; ++b) p0[b] = read_p(stage, 0, b);
+          for (int s = 0; s < kHalves; s += 2) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) q0[n] = read_q(stage, 0, n);
-          mul(p1, q1);
+            for (int b = 0; b < PB; ++b) p0[b] = read_p(stage, s, b);
 #pragma unroll
-          for (int b = 0; b < PB; ++b) p1[b] = read_p(stage, 1, b);
+            for (int n = 0; n < N; ++n) q0[n] = read_q(stage, s, n);
+            mul(p1, q1);
 #pragma unroll
-          for (int n = 0; n < N; ++n) q1[n] = read_q(stage, 1, n);
-          mul(p0, q0);
+            for (int b = 0; b < PB; ++b) p1[b] = read_p(stage, s + 1, b);
+#pragma unroll
+            for (int n = 0; n < N; ++n) q1[n] = read_q(stage, s + 1, n);
+            mul(p0, q0);
+          }
         }
         slot = slot == kSlots - 1 ? 0 : slot + 1;
       }
@@ -555,6 +583,21 @@ __global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product
     stores = GATED ? (a.gu != nullptr ? 6 : 2) * NQ : (a.out_dtype == MOE_DTYPE_FP32 ? 8 : 4) * NQ;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads write this block's LDS
+}
+
+template <int T, int STEP, int MODE, bool GATED, int DT>
+__global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_product_kernel(TileArgs a) {
+  tile_product<T, STEP, MODE, GATED, DT>(a, TileShare{0, 0});
+}
+
+// Both gradients: the matrices' tiles, then the rows', which fill up what the first leave
+// of the card.
+template <int T, int STEP, int DT>
+__global__ __launch_bounds__(tile_threads(T), T == 64 ? 1 : 2) void tile_gradients_kernel(TileArgs mat, TileArgs row,
+                                                                                          TileShare share) {
+  tile_product<T, STEP, kMatGrad, false, DT>(mat, TileShare{0, 0});
+  __syncthreads();  // both use the same LDS
+  tile_product<T, STEP, kRowGrad, false, DT>(row, share);
 }
 
 }  // namespace moe
