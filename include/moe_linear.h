@@ -79,8 +79,9 @@ int moe_linear_grouped(const void* x_dev, const int32_t* offsets_dev, const void
  *       expert owns are left as they were)
  *   dw[e, n, k] = sum over the rows m of e of dout[m, n] x[m, k]  (out_dtype;
  *       zeros for an expert without rows)
- * dx_dev or dw_dev NULL: not computed (and w, or x, may be NULL). Besides the
- * above MOE_ERR_UNSUPPORTED: E * (N / 256 + 1) * (K / 256 + 1) >= 2^30.
+ * dx_dev or dw_dev NULL: not computed (and w, or x, may be NULL), the other
+ * with the same bits. Besides the above MOE_ERR_UNSUPPORTED: (M / 16 + E + 1) *
+ * (K / 16 + 1) >= 2^30.
  */
 int moe_linear_grouped_backward(const void* dout_dev, const void* x_dev, const int32_t* offsets_dev,
                                 const void* w_dev, const moe_linear_shape* shape, void* dx_dev,

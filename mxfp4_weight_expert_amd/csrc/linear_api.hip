@@ -126,7 +126,8 @@ int forward(const Product& p, const void* x, const int32_t* offsets, const void*
 // What both backward passes ask of their shape.
 int check_backward(const Product& p, const int32_t* offsets) {
   if (p.ldx != 0 || p.ldo != 0 || (offsets == nullptr && p.E != 1)) return MOE_ERR_INVALID;
-  if (p.E * (p.N / 256 + 1) * (p.K / 256 + 1) >= kMaxTileItems) return MOE_ERR_UNSUPPORTED;
+  // tiles of the rows' gradient (those of the matrices' are below by N * K and E)
+  if ((p.M / 16 + p.E + 1) * (p.K / 16 + 1) >= kMaxTileItems) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

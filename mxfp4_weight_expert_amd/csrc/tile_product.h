@@ -64,9 +64,12 @@ __device__ __forceinline__ f32x16_t mfma32(uint4 a, uint4 b, f32x16_t c) {
 // does not wait for every load in flight before each LDS read; it has no output
 // registers, and the caller waits (vmcnt) before the barrier that publishes it.
 __device__ __forceinline__ void load_to_lds(uint64_t base, uint32_t off, uint32_t lds) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base >> 32));
-  const i32x4_t rsrc = {static_cast<int>(lo), static_cast<int>(hi & 0xffffu), static_cast<int>(kNoRow), 0x00020000};
+  // the address as scalar instructions' results: one that a vector instruction wrote would
+  // need wait states before the load
+  uint32_t lo, hi;
+  asm("s_mov_b32 %0, %1" : "=s"(lo) : "s"(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base))));
+  asm("s_and_b32 %0, %1, 0xffff" : "=s"(hi) : "s"(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(base >> 32))) : "scc");
+  const i32x4_t rsrc = {static_cast<int>(lo), static_cast<int>(hi), static_cast<int>(kNoRow), 0x00020000};
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(rsrc)
