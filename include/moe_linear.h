@@ -153,7 +153,8 @@ int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32
  *                 for K / N / N; ldx a multiple of 8; each up to 2^20
  *
  * t is held in 32 bits and enters the second product as two values of dtype
- * whose sum is t to 2^-16 of it or better (of the row's largest |t| in fp16).
+ * whose sum is t to 2^-16 of it or better (of the row's largest |t| in fp16),
+ * or three, to 2^-24, where dtype is bf16 and out_dtype fp32.
  */
 typedef struct moe_adapter_shape {
   int32_t M;

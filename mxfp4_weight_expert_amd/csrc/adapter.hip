@@ -2,7 +2,12 @@
 //   out[m, n] = base[m, n] + s[i] * sum over r of t[m, r] B[i, n, r],
 //   t[m, r]   = sum over k of x[m, k] A[i, r, k],   i the adapter of row m.
 // With few rows an adapter memory bounds it: A and B of the adapters that rows
-// have, once each, and base and out.
+// have, once each, and base and out; a handful of rows the two launches one after the
+// other (1 row, rank 16, K 7168, N 2048: 4.3 and 4.7 us). 8191 rows, 8 adapters of rank
+// 64, K 3584, N 7168: 27 us and 78, of which x alone takes 12 at the rate of a large copy
+// and base and out 48; the rest are the parts of t, and A and B, which each XCD reads for
+// itself (218 MB read where base has 117). Spans of N by XCD, so that each reads its part of
+// B alone, and non-temporal base and out gained nothing or lost (108 us, 116).
 //
 // Two launches. The first makes t: a block takes 16 (or 64) sorted rows of one
 // adapter and a part of K, so that few rows still spread over the card; the parts
@@ -342,7 +347,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int
   }
 }
 
-// Rows of an adapter that a tile takes: 64 where M / A says many. Tiles there are at
+// Rows of an adapter that a tile takes: 64 where M / A says many, so that A and B come from
+// L2 a quarter as often. Tiles there are at
 // most one for each row, and one for each adapter beside the full ones.
 bool many_rows(int64_t M, int64_t A) { return M >= 32 * A; }
 int64_t tile_bound(const AdapterArgs& a) {
@@ -398,10 +404,14 @@ void both(const AdapterArgs& a, hipStream_t st) {
 
 }  // namespace
 
+// Parts of K: blocks for two rounds of the card with tiles of 64 rows, whose waves
+// have one step in flight, one round with tiles of 16, where every part is
+// also one more to sum (64 requests 11.5 us, 12.2 with two; 8191 rows 113, 120 with one).
 int adapter_splits(int64_t M, int64_t A, int64_t K) {
-  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(M, M / (many_rows(M, A) ? 64 : 16) + std::min(A, M)));
+  const bool many = many_rows(M, A);
+  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(M, M / (many ? 64 : 16) + std::min(A, M)));
   const int64_t steps = (K + 63) / 64 / kWaves;  // a wave's, unsplit
-  return static_cast<int>(std::clamp<int64_t>(std::min(512 / tiles, steps / 2), 1, 16));
+  return static_cast<int>(std::clamp<int64_t>(std::min((many ? 512 : 256) / tiles, steps / 2), 1, 16));
 }
 
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t st) {

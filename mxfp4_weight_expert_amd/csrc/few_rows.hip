@@ -1,5 +1,9 @@
 // Forward products of 16-bit matrices for few rows (decode): out[m, n] = sum over k of
-// x[m, k] w[e, n, k], or the gated product. The matrices bound it, read once.
+// x[m, k] w[e, n, k], or the gated product. The matrices bound it, read once: 64 tokens
+// of 16 of 896 experts, K 3584 x 2 N 384 gated 563 us, 6.0 TB/s, K 384 x N 3584 295, 5.7 (a
+// large copy reaches 4.9); one token, K 7168 x 2 N 2048 12.9, 4.6, as few blocks hold little
+// in flight. Tokens of an expert share its matrix through L2, so the reads are cached
+// (non-temporal ones 679 us where these take 584).
 //
 // Weights go from global memory straight into the 16x16x32 MFMA as its rows, 16 rows x 64
 // bytes a load, tokens as its columns (from the caches: a few rows of x). A task is a
@@ -196,6 +200,9 @@ void few_go(const TileArgs& a, int kw, hipStream_t st) {
                      dim3(64 * W), 0, st, a, kw);
 }
 
+// Where the weight groups would not fill the card four times over, one group a task, and the
+// waves split K if each then has three steps or more; else tasks of two groups (K of 768 on,
+// split) or four a wave, which read x less often.
 template <int DT, bool GATED>
 void few_size(const TileArgs& a, hipStream_t st) {
   const int64_t groups = (a.R + (GATED ? 7 : 15)) / (GATED ? 8 : 16);

@@ -39,7 +39,7 @@ def _spans(off, M):
 SHAPES = [  # M, E, N, K
     (9000, 40, 2048, 520), (3000, 24, 1288, 2312), (1000, 40, 1536, 1000), (2500, 1, 5128, 4104), (7000, 1, 4616, 4616),
     (300, 12, 2048, 1024), (5000, 2, 1032, 2056), (4000, 1, 2056, 2056), (40, 40, 1000, 1032), (40, 40, 1000, 520),
-    (3, 1, 4096, 2056), (2048, 4, 392, 1544),
+    (3, 1, 4096, 2056), (2048, 4, 392, 1544), (5800, 19, 368, 5152),
 ]
 
 
