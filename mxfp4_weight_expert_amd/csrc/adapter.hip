@@ -4,12 +4,11 @@
 // With few rows an adapter memory bounds it: A and B of the adapters that rows
 // have, once each, and base and out; a handful of rows the two launches one after the
 // other (1 row, rank 16, K 7168, N 2048: 4.3 and 4.7 us). 8191 rows, 8 adapters of rank
-// 64, K 3584, N 7168: 27 us and 78, of which x alone takes 12 at the rate of a large copy
-// and base and out 48; the rest are the parts of t, and A and B, which each XCD reads for
-// itself (218 MB read where base has 117). Spans of N by XCD, so that each reads its part of
-// B alone, and non-temporal base and out gained nothing or lost (108 us, 116).
+// 64, K 3584, N 7168: 28 us and 83, where x alone takes 12 at the rate of a large copy and
+// base and out 48 (140 MB read, 118 written). Spans of N by XCD, so that each reads its part
+// of B alone, and non-temporal base and out gained nothing or lost (108 us, 116).
 //
-// Two launches. The first makes t: a block takes 16 (or 64) sorted rows of one
+// Two launches. The first makes t: a block takes 16 (or 32) sorted rows of one
 // adapter and a part of K, so that few rows still spread over the card; the parts
 // are summed, in order, by the second, whose blocks take the same rows and a span
 // of N. Both read their operands from global memory straight into the 16x16x32
@@ -347,42 +346,49 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int
   }
 }
 
-// Rows of an adapter that a tile takes: 64 where M / A says many, so that A and B come from
-// L2 a quarter as often. Tiles there are at
-// most one for each row, and one for each adapter beside the full ones.
-bool many_rows(int64_t M, int64_t A) { return M >= 32 * A; }
-int64_t tile_bound(const AdapterArgs& a) {
-  const int tr = many_rows(a.M, a.A) ? 64 : 16;
-  return std::min<int64_t>(a.M, a.M / tr + a.A);
-}
+// Sixteens of rows that a tile takes. Two halve the reads of A and B from the caches, which
+// pays for long rows of t and rows enough to fill the card all the same (8192 rows of 2
+// adapters, K 3584, N 4096: rank 64 61 us, four sixteens 73; rank 128 89, 134 with one; rank
+// 8 45, 44 with one; 2683 rows of 16, K 808, N 1456, rank 32: 14.5, 12.0 with one).
+int tile_rows(int64_t M, int64_t A, int64_t R) { return M >= 32 * A && R > 16 && M * R >= 100000 ? 2 : 1; }
+
+// Tiles there are at most one for each row, and one for each adapter beside the full ones.
+int64_t tile_bound(const AdapterArgs& a, int tr) { return std::min<int64_t>(a.M, a.M / (16 * tr) + std::min(a.A, a.M)); }
 
 template <int DT, int RB>
 void down(const AdapterArgs& a, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(tile_bound(a)), static_cast<unsigned>(a.splits));
-  if (many_rows(a.M, a.A))
-    hipLaunchKernelGGL((adapter_down_kernel<DT, RB, 4>), grid, dim3(kThreads), 0, st, a);
+  const int tr = tile_rows(a.M, a.A, a.R);
+  const dim3 grid(static_cast<unsigned>(tile_bound(a, tr)), static_cast<unsigned>(a.splits));
+  if (tr == 2)
+    hipLaunchKernelGGL((adapter_down_kernel<DT, RB, 2>), grid, dim3(kThreads), 0, st, a);
   else
     hipLaunchKernelGGL((adapter_down_kernel<DT, RB, 1>), grid, dim3(kThreads), 0, st, a);
 }
 
 template <int DT, int OT, int RS>
 void up(const AdapterArgs& a, hipStream_t st) {
-  const bool many = many_rows(a.M, a.A);
-  const int tr = many ? 64 : 16;
-  const int64_t tiles = tile_bound(a);
+  const int tr = tile_rows(a.M, a.A, a.R);
+  const int64_t tiles = tile_bound(a, tr);
   // rows without an adapter need a copy only where out is not base
-  const int64_t others = a.out == a.base ? 0 : (a.M + tr - 1) / tr;
-  const int64_t n64 = (a.N + 63) / 64;
-  // spans of N: enough blocks for the card, each with at least one piece a wave
-  const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(tiles, 1));
-  const int64_t per = std::max<int64_t>(kWaves, (n64 + want - 1) / want);
-  const int span = static_cast<int>((per + kWaves - 1) / kWaves * kWaves * 64);
-  const int spans = (a.N + span - 1) / span;
+  const int64_t others = a.out == a.base ? 0 : (a.M + 16 * tr - 1) / (16 * tr);
+  // Spans of N: about four blocks a CU, of a piece a wave or more, and all of one length
+  // where that is not under half of it (4096 rows of 32 adapters, K 3584, N 4096, rank 64:
+  // 43 us, 49 with a shorter last one).
+  const int64_t pieces = (a.N + 64 * kWaves - 1) / (64 * kWaves);
+  const int64_t want = std::clamp<int64_t>(1024 / std::max<int64_t>(tiles, 1), 1, pieces);
+  int64_t per = (pieces + want - 1) / want;
+  for (int64_t p = per; p >= (per + 1) / 2; --p) {
+    if (pieces % p != 0) continue;
+    per = p;
+    break;
+  }
+  const int span = static_cast<int>(per) * kWaves * 64;
+  const int spans = (a.N + span - 1) / span, count = static_cast<int>(tiles);
   const dim3 grid(static_cast<unsigned>((tiles + others) * spans));
-  if (many)
-    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 4>), grid, dim3(kThreads), 0, st, a, static_cast<int>(tiles), span, spans);
+  if (tr == 2)
+    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 2>), grid, dim3(kThreads), 0, st, a, count, span, spans);
   else
-    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 1>), grid, dim3(kThreads), 0, st, a, static_cast<int>(tiles), span, spans);
+    hipLaunchKernelGGL((adapter_up_kernel<DT, OT, RS, 1>), grid, dim3(kThreads), 0, st, a, count, span, spans);
 }
 
 template <int DT, int OT>
@@ -404,14 +410,14 @@ void both(const AdapterArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Parts of K: blocks for two rounds of the card with tiles of 64 rows, whose waves
-// have one step in flight, one round with tiles of 16, where every part is
-// also one more to sum (64 requests 11.5 us, 12.2 with two; 8191 rows 113, 120 with one).
-int adapter_splits(int64_t M, int64_t A, int64_t K) {
-  const bool many = many_rows(M, A);
-  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(M, M / (many ? 64 : 16) + std::min(A, M)));
+// Parts of K: a block a CU, or with tiles of 32 rows two, as these load more than a wave
+// holds in flight; every part is also one more of t to sum (64 requests 11.5 us, 12.2 with
+// twice the parts; 4096 rows of 32 adapters, rank 64: 49, 54 with half of them).
+int adapter_splits(int64_t M, int64_t A, int64_t K, int64_t R) {
+  const int tr = tile_rows(M, A, R);
+  const int64_t tiles = std::max<int64_t>(1, std::min<int64_t>(M, M / (16 * tr) + std::min(A, M)));
   const int64_t steps = (K + 63) / 64 / kWaves;  // a wave's, unsplit
-  return static_cast<int>(std::clamp<int64_t>(std::min((many ? 512 : 256) / tiles, steps / 2), 1, 16));
+  return static_cast<int>(std::clamp<int64_t>(std::min(tr > 1 ? 512 / tiles : (255 + tiles) / tiles, steps / 2), 1, 16));
 }
 
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t st) {

@@ -203,7 +203,7 @@ struct AdapterArgs {
   int64_t ldx, ldb, ldo;
 };
 // Parts of K that the first product is split into.
-int adapter_splits(int64_t M, int64_t A, int64_t K);
+int adapter_splits(int64_t M, int64_t A, int64_t K, int64_t R);
 hipError_t launch_adapter(const AdapterArgs& a, hipStream_t st);
 
 hipError_t launch_prepack(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t row_bytes,

@@ -171,7 +171,7 @@ int check(const moe_adapter_shape* s) {
 
 // t by part of K; the maps' workspace where it is larger.
 uint64_t adapter_ws(const moe_adapter_shape& s) {
-  const uint64_t part = static_cast<uint64_t>(adapter_splits(s.M, s.A, s.K)) * s.M * s.R * 4;
+  const uint64_t part = static_cast<uint64_t>(adapter_splits(s.M, s.A, s.K, s.R)) * s.M * s.R * 4;
   const uint64_t both = part > maps_ws(s.M, s.A).bytes ? part : maps_ws(s.M, s.A).bytes;
   return (both + 255) / 256 * 256;
 }
@@ -245,7 +245,7 @@ int moe_linear_adapter(const void* x_dev, const int32_t* offsets_dev, const int3
   const bool same = base_dev == out_dev && ldb == ldo;
   if (base_dev != nullptr && !same && rows_overlap(base_dev, N * so, ldb * so, out_dev, N * so, ldo * so, M))
     return MOE_ERR_INVALID;
-  const int splits = adapter_splits(M, A, s.K);
+  const int splits = adapter_splits(M, A, s.K, s.R);
   const int64_t bytes = splits * M * R * 4;
   if (workspace_dev == nullptr || !aligned(workspace_dev, 256) || workspace_bytes < static_cast<uint64_t>(bytes))
     return MOE_ERR_WORKSPACE;

@@ -72,8 +72,8 @@ def test_maps_of_many_rows():
         assert np.array_equal(off, ro) and np.array_equal(row_slot[:ro[-1]], rr) and np.array_equal(slot_row, rs[:, 0])
 
 
-# few rows of many adapters; tiles of 16 with full, partial and following ones; of 64;
-# more adapters than a block has threads
+# few rows of many adapters; tiles with full, partial and following ones; more adapters
+# than a block has threads
 ROWS = [(1, 1), (3, 40), (50, 4), (90, 300), (33, 1), (70, 2), (400, 3)]
 
 
@@ -89,6 +89,22 @@ def test_adapters(M, A, N, K, R, dtype, out):
     close(got, ref, round_tol(ref, out, tol), "out")
     assert torch.equal(got[ids < 0], t["base"][ids < 0])
     # in place
+    own = t["base"].clone()
+    assert _run(ids, t, shape, base=own, out=own) is own and torch.equal(own, got)
+
+
+# tiles of 32 rows, an adapter's last one partial; spans of N of several pieces, a short last one
+@pytest.mark.parametrize("M,A,N,K,R", [(4300, 3, 70, 264, 24), (3300, 100, 1030, 72, 32), (1601, 50, 2057, 520, 64),
+                                       (1601, 1, 513, 1032, 72), (1025, 7, 1100, 2056, 128), (9001, 9, 776, 40, 128)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16")])
+def test_adapters_of_many_rows(M, A, N, K, R, dtype, out):
+    say(f"[adapter] {M} {A} {N} {K} {R} {dtype} {out}")
+    rng = np.random.default_rng(M + N)
+    ids, t, shape = _case(rng, M, N, K, R, A, dtype, out, none=0.1)
+    ref, tol = _want(ids, t)
+    got = _run(ids, t, shape)
+    close(got, ref, round_tol(ref, out, tol), "out")
+    assert torch.equal(got[ids < 0], t["base"][ids < 0])
     own = t["base"].clone()
     assert _run(ids, t, shape, base=own, out=own) is own and torch.equal(own, got)
 
