@@ -348,7 +348,7 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int
 
 // Sixteens of rows that a tile takes. Two halve the reads of A and B from the caches, which
 // pays for long rows of t and rows enough to fill the card all the same (8192 rows of 2
-// adapters, K 3584, N 4096: rank 64 61 us, four sixteens 73; rank 128 89, 134 with one; rank
+// adapters, K 3584, N 4096: rank 64 61 us, four sixteens 73; rank 128 93, 134 with one; rank
 // 8 45, 44 with one; 2683 rows of 16, K 808, N 1456, rank 32: 14.5, 12.0 with one).
 int tile_rows(int64_t M, int64_t A, int64_t R) { return M >= 32 * A && R > 16 && M * R >= 100000 ? 2 : 1; }
 
@@ -373,9 +373,11 @@ void up(const AdapterArgs& a, hipStream_t st) {
   const int64_t others = a.out == a.base ? 0 : (a.M + 16 * tr - 1) / (16 * tr);
   // Spans of N: about four blocks a CU, of a piece a wave or more, and all of one length
   // where that is not under half of it (4096 rows of 32 adapters, K 3584, N 4096, rank 64:
-  // 43 us, 49 with a shorter last one).
+  // 43 us, 49 with a shorter last one); eight where tiles of 32 rows alone make one, whose
+  // shorter spans then lie nearer to each other in memory (8191 rows of 8 adapters, rank 64,
+  // K 3584, N 7168: 105 us, 120 with four).
   const int64_t pieces = (a.N + 64 * kWaves - 1) / (64 * kWaves);
-  const int64_t want = std::clamp<int64_t>(1024 / std::max<int64_t>(tiles, 1), 1, pieces);
+  const int64_t want = std::clamp<int64_t>((tr == 2 && tiles >= 256 ? 2048 : 1024) / std::max<int64_t>(tiles, 1), 1, pieces);
   int64_t per = (pieces + want - 1) / want;
   for (int64_t p = per; p >= (per + 1) / 2; --p) {
     if (pieces % p != 0) continue;
