@@ -4,8 +4,8 @@
 // With few rows an adapter memory bounds it: A and B of the adapters that rows
 // have, once each, and base and out; a handful of rows the two launches one after the
 // other (1 row, rank 16, K 7168, N 2048: 4.3 and 4.7 us). 8191 rows, 8 adapters of rank
-// 64, K 3584, N 7168: 28 us and 83, where x alone takes 12 at the rate of a large copy and
-// base and out 48 (140 MB read, 118 written). Spans of N by XCD, so that each reads its part
+// 64, K 3584, N 7168: 27 us and 77, where x alone takes 12 at the rate of a large copy and
+// base and out 48 (191 MB read, 118 written). Spans of N by XCD, so that each reads its part
 // of B alone, and non-temporal base and out gained nothing or lost (108 us, 116).
 //
 // Two launches. The first makes t: a block takes 16 (or 32) sorted rows of one
@@ -251,7 +251,8 @@ __global__ __launch_bounds__(kThreads) void adapter_up_kernel(AdapterArgs a, int
       for (int i = 0; i < kPieces; ++i) {
         const int at = n + col(i * kVec / 4, q);
         old[m][i] = uint4{0u, 0u, 0u, 0u};
-        if (base != nullptr && row[m] >= 0 && at < n1) old[m][i] = load_piece<OT>(base + (row[m] * a.ldb + at) * OS, n1 - at);
+        if (base != nullptr && row[m] >= 0 && at < n1)
+          old[m][i] = load_piece<OT>(base + (row[m] * a.ldb + at) * OS, n1 - at);
       }
   };
   int n = n0 + wv * 64;
@@ -375,7 +376,7 @@ void up(const AdapterArgs& a, hipStream_t st) {
   // where that is not under half of it (4096 rows of 32 adapters, K 3584, N 4096, rank 64:
   // 43 us, 49 with a shorter last one); eight where tiles of 32 rows alone make one, whose
   // shorter spans then lie nearer to each other in memory (8191 rows of 8 adapters, rank 64,
-  // K 3584, N 7168: 105 us, 120 with four).
+  // K 3584, N 7168: 105 us, 113 with four).
   const int64_t pieces = (a.N + 64 * kWaves - 1) / (64 * kWaves);
   const int64_t want = std::clamp<int64_t>((tr == 2 && tiles >= 256 ? 2048 : 1024) / std::max<int64_t>(tiles, 1), 1, pieces);
   int64_t per = (pieces + want - 1) / want;
