@@ -94,7 +94,8 @@ int moe_linear_grouped_backward(const void* dout_dev, const void* x_dev, const i
  *   M, E, dtype  as above (x, w13, h, the pre-activations and all gradients)
  *   I, H         features of h and elements of a row of x, multiples of 8
  *   activation, swiglu_limit, act_beta, act_linear_beta
- *                as in moe_mxfp4_shape; the sums enter it in 32 bits
+ *                as in moe_mxfp4_shape; the sums enter it in 32 bits. The clamp of
+ *                swiglu_limit cuts infinities off and leaves NaN NaN
  *   ldx, ldo     elements from one row of x / h to the next, multiples of 8; 0
  *                stands for H / I. The backward pass takes 0 alone.
  */
@@ -126,7 +127,8 @@ int moe_linear_gated(const void* x_dev, const int32_t* offsets_dev, const void* 
 /*
  * Gradients from dh [M, I] at the pre-activations gu [M, 2 I]:
  *   dgu[m, (g, u)] = dh times the derivative of act, rounded to dtype; 0 where
- *       the clamp of swiglu_limit > 0 cut off (g > L, |u| > L)
+ *       the clamp of swiglu_limit > 0 cut off (g > L, |u| > L; on the limit and
+ *       for NaN it does not)
  *   dx = dgu w13 and dw13 = dgu^T x, as moe_linear_grouped_backward
  * dgu_dev [M, 2 I] is written, and read, in the rows that experts own: the
  * caller's scratch, or the gradient of the pre-activations. dx_dev or dw_dev

@@ -115,7 +115,7 @@ extern "C" {
  *                   scaled f8f6f4 MFMA with the E2M1 weights fed as they are
  *   force_gemm2_path  MOE_GEMM2_AUTO, _SPLIT or _DENSE
  *   swiglu_limit    > 0: gate = min(gate, L), up = clamp(up, -L, L)
- *                   before silu(gate) * up; <= 0: no clamp
+ *                   before silu(gate) * up (NaN stays NaN); <= 0: no clamp
  *   shared_scale    multiplier of the shared-expert sigmoid (1/ep_size on
  *                   the page; 1.0 on one GPU)
  *   act_beta        SiTU gate cap beta (> 0, finite; the K3.1 value is 4)

@@ -20,10 +20,10 @@ __device__ __forceinline__ void act_grad(float dh, float g, float u, const ActAr
   }
   bool in_g = true, in_u = true;
   if (a.limit > 0.0f) {
-    in_g = g <= a.limit;
-    in_u = fabsf(u) <= a.limit;
-    g = fminf(g, a.limit);
-    u = fminf(fmaxf(u, -a.limit), a.limit);
+    in_g = !(g > a.limit);  // NaN is not cut off
+    in_u = !(fabsf(u) > a.limit);
+    g = clamp_gate(g, a.limit);
+    u = clamp_up(u, a.limit);
   }
   const float s = 1.0f / (1.0f + __expf(-g));
   dg = in_g ? dh * u * (s * (1.0f + g * (1.0f - s))) : 0.0f;

@@ -287,10 +287,18 @@ __device__ __forceinline__ float act_apply(float g, float u, const ActArgs& a) {
   return swiglu(g, u, a.limit);
 }
 
+// The clamp of the gate and up halves. NaN stays NaN: fminf and fmaxf would make a number
+// of it, the limit.
+__device__ __forceinline__ float clamp_gate(float g, float limit) {
+  return __builtin_elementwise_minimum(g, limit);
+}
+__device__ __forceinline__ float clamp_up(float u, float limit) {
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(u, -limit), limit);
+}
 __device__ __forceinline__ float swiglu(float g, float u, float limit) {
   if (limit > 0.0f) {
-    g = fminf(g, limit);
-    u = fminf(fmaxf(u, -limit), limit);
+    g = clamp_gate(g, limit);
+    u = clamp_up(u, limit);
   }
   return silu_f(g) * u;
 }
