@@ -212,6 +212,13 @@ def _gradient(t, shape: tuple, dtype, like):
     return ops.torch.empty(shape, dtype=dtype, device=like.device) if t is None else t
 
 
+def _given(t, what: str, gradient, name: str) -> bool:
+    """Whether an operand is there; the one that a wanted gradient reads has to be."""
+    if t is None and gradient is not False:
+        raise ValueError(f"{what} is needed for {name}")
+    return t is not None
+
+
 def grouped_linear_backward(dout, x, offsets, w, shape: LinearShape, *, dx=None, dw=None, stream=None):
     """Gradients of grouped_linear from dout [M, N] in shape.dtype: (dx [M, K],
     dw [E, N, K] in shape.out_dtype). Rows of dx that no expert owns stay as they
@@ -225,8 +232,8 @@ def grouped_linear_backward(dout, x, offsets, w, shape: LinearShape, *, dx=None,
     rows, result, matrices = shape._arrays
     gpu = dout.get_device()
     pd, po = _check(dout, "dout", result, dt, gpu), _offsets(offsets, shape.E, gpu)
-    px = None if x is None and dw is False else _check(x, "x", rows, dt, gpu)
-    pw = None if w is None and dx is False else _matrices(w, "w", matrices, dt, gpu)
+    px = _check(x, "x", rows, dt, gpu) if _given(x, "x", dw, "dw") else None
+    pw = _matrices(w, "w", matrices, dt, gpu) if _given(w, "w", dx, "dx") else None
     dx, dw = _gradient(dx, rows, dt, dout), _gradient(dw, matrices, odt, dout)
     _run("grouped_backward", gpu, pd, px, po, pw, shape._c, None if dx is None else _check(dx, "dx", rows, dt, gpu),
          None if dw is None else _matrices(dw, "dw", matrices, odt, gpu))
@@ -274,8 +281,8 @@ def gated_linear_backward(dh, x, offsets, gu, w13, shape: GatedShape, *, dx=None
     rows, result, pre, matrices = shape._arrays
     gpu = dh.get_device()
     pd, po, pg = _check(dh, "dh", result, dt, gpu), _offsets(offsets, shape.E, gpu), _check(gu, "gu", pre, dt, gpu)
-    px = None if x is None and dw is False else _check(x, "x", rows, dt, gpu)
-    pw = None if w13 is None and dx is False else _matrices(w13, "w13", matrices, dt, gpu)
+    px = _check(x, "x", rows, dt, gpu) if _given(x, "x", dw, "dw") else None
+    pw = _matrices(w13, "w13", matrices, dt, gpu) if _given(w13, "w13", dx, "dx") else None
     if dgu is None:
         dgu = ops.torch.empty(pre, dtype=dt, device=dh.device)
     dx, dw = _gradient(dx, rows, dt, dh), _gradient(dw, matrices, dt, dh)
