@@ -2,7 +2,8 @@
 // pre-activations g, u of the rows that experts own. Elementwise; memory bounds
 // it: three arrays read and two written, M * I elements each (8192 rows, I 2048, bf16: 168
 // MB in 29 us, 5.8 TB/s, a large copy 4.9). dgu is rounded before the products that take
-// it, which read it as 16-bit operands.
+// it, which read it as 16-bit operands; what the rounding leaves goes to an array of its
+// own where the caller asks for two terms, and the products take both.
 #include "rows.h"
 #include "kernels.h"
 
@@ -30,6 +31,19 @@ __device__ __forceinline__ void act_grad(float dh, float g, float u, const ActAr
   du = in_u ? dh * (g * s) : 0.0f;
 }
 
+// Eight values rounded, and what is left of each (nothing beside an infinity or NaN).
+template <int DT>
+__device__ __forceinline__ void store_terms(const float* v, uint16_t* to, uint16_t* rest) {
+  const uint4 p = Row<DT>::pack(v);
+  *reinterpret_cast<uint4*>(to) = p;
+  if (rest == nullptr) return;
+  float r[8];
+  Row<DT>::unpack(p, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = fabsf(r[i]) < __builtin_inff() ? v[i] - r[i] : 0.0f;
+  *reinterpret_cast<uint4*>(rest) = Row<DT>::pack(r);
+}
+
 template <int DT>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   int lo = 0, hi = a.M;
@@ -42,6 +56,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   const uint16_t* const dh = static_cast<const uint16_t*>(a.dh);
   const uint16_t* const gu = static_cast<const uint16_t*>(a.gu);
   uint16_t* const out = static_cast<uint16_t*>(a.dgu);
+  uint16_t* const rest = static_cast<uint16_t*>(a.rest);
   for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n; at += step) {
     const int64_t row = lo + at / pieces;
     const int i = static_cast<int>(at % pieces) * 8;
@@ -51,8 +66,9 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
     Row<DT>::unpack(ld16(gu + row * 2 * a.I + a.I + i), u);
 #pragma unroll
     for (int v = 0; v < 8; ++v) act_grad(d[v], g[v], u[v], a.act, dg[v], du[v]);
-    *reinterpret_cast<uint4*>(out + row * 2 * a.I + i) = Row<DT>::pack(dg);
-    *reinterpret_cast<uint4*>(out + row * 2 * a.I + a.I + i) = Row<DT>::pack(du);
+    const int64_t to = row * 2 * a.I + i;
+    store_terms<DT>(dg, out + to, rest != nullptr ? rest + to : nullptr);
+    store_terms<DT>(du, out + to + a.I, rest != nullptr ? rest + to + a.I : nullptr);
   }
 }
 

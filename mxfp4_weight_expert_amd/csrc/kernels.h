@@ -167,6 +167,8 @@ struct TileArgs {
   int64_t pstride;         // elements from one matrix of P to the next
   int64_t ldp, ldq, ldo;   // elements from row to row
   int dtype, out_dtype;
+  int terms;               // gradients: arrays whose sum Q is, 1 or 2
+  int64_t qterm;           // elements from one of them to the next
   ActArgs act;             // gated
 };
 hipError_t launch_tile_forward(const TileArgs& a, bool gated, hipStream_t st);
@@ -180,6 +182,7 @@ struct ActGradArgs {
   const void* dh;
   const void* gu;
   void* dgu;
+  void* rest;              // [M, 2 I], what dgu's rounding left, or null
   const int32_t* offsets;  // or null
   int M, I, E, dtype;
   ActArgs act;

@@ -45,7 +45,7 @@ int check(const moe_gated_shape* s, Product& p) {
   if (s == nullptr || s->I < 1) return MOE_ERR_INVALID;
   p = {s->M, int64_t{2} * s->I, s->H, s->E, s->ldx, s->ldo, s->I, s->dtype, s->dtype};
   const bool situ = s->activation == MOE_ACT_SITU;
-  if (!std::isfinite(s->swiglu_limit)) return MOE_ERR_INVALID;
+  if (!std::isfinite(s->swiglu_limit) || s->dgu_terms < 0 || s->dgu_terms > 2) return MOE_ERR_INVALID;
   if (situ && !(std::isfinite(s->act_beta) && s->act_beta > 0.0f && std::isfinite(s->act_linear_beta) &&
                 s->act_linear_beta > 0.0f))
     return MOE_ERR_INVALID;
@@ -92,6 +92,7 @@ TileArgs tile_args(const Product& p, const int32_t* offsets) {
   a.pstride = p.N * p.K;
   a.dtype = p.dtype;
   a.out_dtype = p.dtype;
+  a.terms = 1;
   return a;
 }
 
@@ -131,10 +132,14 @@ int check_backward(const Product& p, const int32_t* offsets) {
   return MOE_OK;
 }
 
-// dx and dw from the gradient of the product, either of them null.
-int gradients(const Product& p, const void* dout, const void* x, const int32_t* offsets, const void* w, void* dx,
-              void* dw, hipStream_t st) {
-  TileArgs row = tile_args(p, offsets), mat = row;
+// dx and dw from the gradient of the product, the sum of `terms` arrays that follow each
+// other; either of them null.
+int gradients(const Product& p, const void* dout, int terms, const void* x, const int32_t* offsets, const void* w,
+              void* dx, void* dw, hipStream_t st) {
+  TileArgs row = tile_args(p, offsets);
+  row.terms = terms;
+  row.qterm = p.M * p.N;
+  TileArgs mat = row;
   row.p = w;
   row.q = dout;
   row.out = dx;
@@ -303,7 +308,7 @@ int moe_linear_grouped_backward(const void* dout_dev, const void* x_dev, const i
                         {w_dev, dx_dev != nullptr ? matrices * 2 : 0},
                         {offsets_dev, offsets_bytes(p)}};
   if (meet(outs, ins)) return MOE_ERR_INVALID;
-  return gradients(p, dout_dev, x_dev, offsets_dev, w_dev, dx_dev, dw_dev, static_cast<hipStream_t>(stream));
+  return gradients(p, dout_dev, 1, x_dev, offsets_dev, w_dev, dx_dev, dw_dev, static_cast<hipStream_t>(stream));
 }
 
 int moe_linear_gated(const void* x_dev, const int32_t* offsets_dev, const void* w13_dev,
@@ -329,7 +334,8 @@ int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32
       !aligned(dgu_dev, 16) || !aligned(dx_dev, 16) || !aligned(dw_dev, 16) || !aligned(offsets_dev, 4))
     return MOE_ERR_INVALID;
   const int64_t matrices = p.E * p.N * p.K * 2, pre = p.M * p.N * 2, rows = p.M * p.K * 2;
-  const Range outs[3] = {{dgu_dev, pre}, {dx_dev, rows}, {dw_dev, matrices}};
+  const int terms = shape->dgu_terms == 2 ? 2 : 1;
+  const Range outs[3] = {{dgu_dev, terms * pre}, {dx_dev, rows}, {dw_dev, matrices}};
   const Range ins[5] = {{dh_dev, pre / 2}, {gu_dev, pre}, {x_dev, dw_dev != nullptr ? rows : 0},
                         {w13_dev, dx_dev != nullptr ? matrices : 0}, {offsets_dev, offsets_bytes(p)}};
   if (meet(outs, ins)) return MOE_ERR_INVALID;
@@ -338,6 +344,7 @@ int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32
     g.dh = dh_dev;
     g.gu = gu_dev;
     g.dgu = dgu_dev;
+    g.rest = terms > 1 ? static_cast<uint8_t*>(dgu_dev) + pre : nullptr;
     g.offsets = offsets_dev;
     g.M = shape->M;
     g.I = shape->I;
@@ -347,7 +354,7 @@ int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32
     rc = status(launch_act_grad(g, static_cast<hipStream_t>(stream)));
     if (rc != MOE_OK) return rc;
   }
-  return gradients(p, dgu_dev, x_dev, offsets_dev, w13_dev, dx_dev, dw_dev, static_cast<hipStream_t>(stream));
+  return gradients(p, dgu_dev, terms, x_dev, offsets_dev, w13_dev, dx_dev, dw_dev, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -45,8 +45,12 @@ template <int T, int STEP, int MODE, bool GATED, int DT>
 hipError_t tile_go(const TileArgs& a, hipStream_t st) {
   const int64_t blocks = std::min((tile_items<T, MODE, GATED>(a) + 7) / 8 * 8, tile_blocks<T>());
   const int lds = tile_room<T, STEP>(a);
-  hipLaunchKernelGGL((tile_product_kernel<T, STEP, MODE, GATED, DT>), dim3(static_cast<unsigned>(blocks)),
-                     dim3(tile_threads(T)), lds, st, a);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(tile_threads(T)), lds, st, a);
+  };
+  if constexpr (MODE == kForward) go(tile_product_kernel<T, STEP, MODE, GATED, DT, 1>);
+  else if (a.terms == 1) go(tile_product_kernel<T, STEP, MODE, GATED, DT, 1>);
+  else go(tile_product_kernel<T, STEP, MODE, GATED, DT, 2>);
   return hipGetLastError();
 }
 // How many tiles of the rows' gradient take as long as one of the matrices'.
@@ -59,8 +63,11 @@ hipError_t tile_gradients_go(const TileArgs& mat, const TileArgs& row, hipStream
   const int64_t blocks = std::min((all + 7) / 8 * 8, tile_blocks<T>());
   const TileShare share = {static_cast<int>(first), static_cast<int>(std::clamp(tile_ratio(mat, row) + 0.5, 0.0, 1024.0))};
   const int lds = tile_room<T, STEP>(mat);
-  hipLaunchKernelGGL((tile_gradients_kernel<T, STEP, DT>), dim3(static_cast<unsigned>(blocks)), dim3(tile_threads(T)),
-                     lds, st, mat, row, share);
+  const auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(tile_threads(T)), lds, st, mat, row, share);
+  };
+  if (mat.terms == 1) go(tile_gradients_kernel<T, STEP, DT, 1>);
+  else go(tile_gradients_kernel<T, STEP, DT, 2>);
   return hipGetLastError();
 }
 
@@ -76,7 +83,7 @@ double tile_time(const TileArgs& a) {
   const int64_t wide = GATED ? T / 2 : T, nr = (a.R + wide - 1) / wide;
   const double across = MODE == kMatGrad ? a.C : rows;
   const double tiles = std::ceil(across / T) * nr * (MODE == kMatGrad ? a.E : std::min<double>(a.E, a.M));
-  const double steps = std::ceil((MODE == kMatGrad ? rows : a.I) / 32), fill = std::min(1.0, across / T);
+  const double steps = std::ceil((MODE == kMatGrad ? rows : a.I) / 32) * a.terms, fill = std::min(1.0, across / T);
   const double rounds = std::ceil(tiles / static_cast<double>(tile_blocks<T>()));
   if (T == 64) return rounds * (2.2 + steps * (tiles <= 128 ? 0.12 : 0.2));
   if (T == 256) return rounds * (7 + steps * (0.45 + 0.4 * fill));

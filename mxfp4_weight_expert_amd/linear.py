@@ -31,7 +31,7 @@ class _LinearShape(ctypes.Structure):
 class _GatedShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "I", "H", "E", "dtype", "activation")] + [
         (n, ctypes.c_float) for n in ("swiglu_limit", "act_beta", "act_linear_beta")] + [
-        ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+        ("dgu_terms", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64)]
 
 
 class _AdapterShape(ctypes.Structure):
@@ -85,12 +85,13 @@ class GatedShape(_Kept):
     swiglu_limit: float = 0.0
     act_beta: float = 4.0  # SiTU caps (read only for "situ")
     act_linear_beta: float = 25.0
-    _sizes = ("M", "I", "H", "E")
+    dgu_terms: int = 1  # 2: the backward pass keeps what rounding dgu leaves
+    _sizes = ("M", "I", "H", "E", "dgu_terms")
 
     def to_c(self, ldx: int = 0, ldo: int = 0) -> _GatedShape:
         self._fits
         return _GatedShape(self.M, self.I, self.H, self.E, DTYPE[self.dtype], ACTIVATION[self.activation],
-                           float(self.swiglu_limit), float(self.act_beta), float(self.act_linear_beta), ldx, ldo)
+                           float(self.swiglu_limit), float(self.act_beta), float(self.act_linear_beta), self.dgu_terms, ldx, ldo)
 
     @functools.cached_property
     def _c(self):
@@ -104,6 +105,10 @@ class GatedShape(_Kept):
     def _arrays(self):
         """Shapes of x, h, the pre-activations and the matrices."""
         return (self.M, self.H), (self.M, self.I), (self.M, 2 * self.I), (self.E, 2 * self.I, self.H)
+
+    @functools.cached_property
+    def _dgu(self):
+        return (self.M, 2 * self.I) if self.dgu_terms <= 1 else (self.dgu_terms, self.M, 2 * self.I)
 
 
 @dataclass(frozen=True)
@@ -271,8 +276,11 @@ def gated_linear(x, offsets, w13, shape: GatedShape, *, out=None, gu=None, strea
 def gated_linear_backward(dh, x, offsets, gu, w13, shape: GatedShape, *, dx=None, dw=None, dgu=None, stream=None):
     """Gradients of gated_linear from dh [M, I] at the pre-activations gu [M, 2 I]:
     (dx [M, H], dw [E, 2 I, H]). dgu [M, 2 I] takes the gradient of the
-    pre-activations in the rows that experts own (made here when None). dx or dw
-    False: not computed, None in its place. All arrays are contiguous.
+    pre-activations in the rows that experts own (made here when None), rounded to
+    shape.dtype before the products that take it; with shape.dgu_terms 2 it is
+    [2, M, 2 I], a sum of two such values, and dx and dw are off by their own
+    rounding alone, in one and a half to two times the time. dx or dw False: not
+    computed, None in its place. All arrays are contiguous.
     """
     dt = shape._torch
     if stream is not None:
@@ -284,9 +292,9 @@ def gated_linear_backward(dh, x, offsets, gu, w13, shape: GatedShape, *, dx=None
     px = _check(x, "x", rows, dt, gpu) if _given(x, "x", dw, "dw") else None
     pw = _matrices(w13, "w13", matrices, dt, gpu) if _given(w13, "w13", dx, "dx") else None
     if dgu is None:
-        dgu = ops.torch.empty(pre, dtype=dt, device=dh.device)
+        dgu = ops.torch.empty(shape._dgu, dtype=dt, device=dh.device)
     dx, dw = _gradient(dx, rows, dt, dh), _gradient(dw, matrices, dt, dh)
-    _run("gated_backward", gpu, pd, px, po, pg, pw, shape._c, _check(dgu, "dgu", pre, dt, gpu),
+    _run("gated_backward", gpu, pd, px, po, pg, pw, shape._c, _check(dgu, "dgu", shape._dgu, dt, gpu),
          None if dx is None else _check(dx, "dx", rows, dt, gpu), None if dw is None else _matrices(dw, "dw", matrices, dt, gpu))
     ops._changed(tuple(t for t in (dgu, dx, dw) if t is not None))
     return dx, dw
