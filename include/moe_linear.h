@@ -164,8 +164,9 @@ int moe_linear_gated_backward(const void* dh_dev, const void* x_dev, const int32
  *                 for K / N / N; ldx a multiple of 8; each up to 2^20
  *
  * t is held in 32 bits and enters the second product as two values of dtype
- * whose sum is t to 2^-16 of it or better (of the row's largest |t| in fp16),
- * or three, to 2^-24, where dtype is bf16 and out_dtype fp32.
+ * whose sum is t to 2^-16 of it in bf16 and in fp16 to 2^-22 of it, or 2^-25 of
+ * the row's largest |t| where that is more; or as three, to 2^-24, where dtype
+ * is bf16 and out_dtype fp32. An infinity in b gives infinities or NaN.
  */
 typedef struct moe_adapter_shape {
   int32_t M;
