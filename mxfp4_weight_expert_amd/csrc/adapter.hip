@@ -375,8 +375,11 @@ void up(const AdapterArgs& a, hipStream_t st) {
   // Spans of N: about four blocks a CU, of a piece a wave or more, and all of one length
   // where that is not under half of it (4096 rows of 32 adapters, K 3584, N 4096, rank 64:
   // 43 us, 49 with a shorter last one); eight where tiles of 32 rows alone make one, whose
-  // shorter spans then lie nearer to each other in memory (8191 rows of 8 adapters, rank 64,
-  // K 3584, N 7168: 105 us, 113 with four).
+  // shorter spans then lie nearer to each other in memory. Eight and four (us): rank 64, K
+  // 3584, N 7168, 8 adapters: 8191 rows 106 and 113, 12000 161 and 176, 16000 202 and 206;
+  // N 4096, 32 adapters: 65 and 64, 119 and 125, 140 and 153. Below 256 tiles: 2048 rows 37
+  // and 34, 6000 68 and 69. Short rows (K 1024, N 2048, 2 adapters) the same, but of rank
+  // 128 from 12000 rows on 68 and 61.
   const int64_t pieces = (a.N + 64 * kWaves - 1) / (64 * kWaves);
   const int64_t want = std::clamp<int64_t>((tr == 2 && tiles >= 256 ? 2048 : 1024) / std::max<int64_t>(tiles, 1), 1, pieces);
   int64_t per = (pieces + want - 1) / want;
